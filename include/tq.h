@@ -337,6 +337,127 @@ int tq_search_topk(const tq_ctx* ctx, const float* q, int64_t nq, const tq_packe
                    int k, float* scores, int64_t* ids, void* workspace, size_t ws_bytes,
                    tq_stream_t stream);
 
+/* ------------------------------------------------------------------ around the cache
+ * tq_rope -- rotary positions of up to two tensors (queries and keys) in one launch, ahead of
+ * tq_quantize_kv, tq_page_bounds and the attention calls.  Pair i of a head of token v turns by
+ * a = pos[v] * freq[i]:
+ *   y1 = factor (x1 cos a - x2 sin a),  y2 = factor (x2 cos a + x1 sin a),  0 <= i < rot/2
+ * with (x1, x2) = channels (i, i + rot/2), or (2i, 2i + 1) with TQ_ROPE_INTERLEAVED; channels
+ * rot..D-1 are copied.  TQ_ROPE_TRANSPOSE turns by -a: the gradient of the call without it (and,
+ * for factor 1, its inverse).  The angle is formed in 64 bits, the products in 32 bits, and the
+ * result is rounded once to the tensors' type.
+ * tensors: host array of ntensors (1 or 2); x and out device, of dtype (F32 / BF16 / F16), channel
+ *   c of head h of token v at x + v*x_token + h*x_head + c (elements; channels are contiguous).
+ *   out may be x with the same strides; any other overlap is undefined.
+ * freq: device double [rot/2]; pos: device int32 or int64 [n] (pos_bits 32 or 64).
+ * Speed: 16-byte aligned pointers and strides, with rot/2 (rot when interleaved) and D - rot
+ *   multiples of 16 bytes, move 16 bytes a thread; other calls give the same results with
+ *   narrower ones.
+ * Errors: TQ_ERR_INVALID_ARG (NULL pointers, negative sizes, rot odd or outside [2, D], bad dtype,
+ *   pos_bits or flags), TQ_ERR_UNSUPPORTED (D > 4096, more than 2^19 elements a token, a pointer
+ *   that is not aligned to its element), TQ_ERR_CUDA. */
+enum tq_rope_flags { TQ_ROPE_INTERLEAVED = 1, TQ_ROPE_TRANSPOSE = 2 };
+typedef struct tq_rope_tensor {
+  const void* x;
+  void* out;
+  int heads;
+  int64_t x_token, x_head;     /* strides in elements */
+  int64_t out_token, out_head;
+} tq_rope_tensor;
+int tq_rope(const tq_rope_tensor* tensors, int ntensors, int dtype, int64_t n, int D, int rot, const double* freq,
+            const void* pos, int pos_bits, double factor, int flags, tq_stream_t stream);
+
+/* tq_rope_frequencies -- host: freq[i] = base^(-2i/rot) of every pair under a long-context rule, and
+ * the factor on the rotated values (1 but for YARN).  s NULL: no rule.
+ *   LINEAR: freq / factor (positions interpolated).
+ *   NTK:    base * factor^(rot/(rot-2)).
+ *   BANDS:  with w = clamp((original_len freq / 2 pi - low) / (high - low), 0, 1):
+ *           freq (w + (1 - w) / factor): pairs with more than `high` turns over the original length
+ *           keep their frequency, those with fewer than `low` are interpolated.
+ *   YARN:   a ramp over the pair index between the pairs with `high` and `low` turns over the
+ *           original length, from freq to freq / factor; factor_out = 0.1 ln(factor) + 1.
+ * Errors: TQ_ERR_INVALID_ARG (NULL pointers, rot odd or < 2, base <= 1, factor <= 0, original_len <= 0
+ * or low >= high where they are used, unknown kind). */
+enum tq_rope_scale { TQ_ROPE_SCALE_NONE = 0, TQ_ROPE_SCALE_LINEAR, TQ_ROPE_SCALE_NTK, TQ_ROPE_SCALE_BANDS,
+                     TQ_ROPE_SCALE_YARN };
+typedef struct tq_rope_scaling {
+  int kind;
+  double factor, original_len, low, high;
+} tq_rope_scaling;
+int tq_rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* freq, double* factor_out);
+
+/* tq_page_bounds -- element-wise bounds of the keys in each page of a paged cache, kept by the caller
+ * next to it: bounds (device, of dtype) is [npages][Hkv][2][D] with the minimum, then the maximum, of
+ * the keys (rows as given to tq_quantize_kv) of page p and kv head h.  The call folds in new rows:
+ * sequence b (B of them) appends rows cu_new[b] .. cu_new[b+1]-1 of k as its tokens start[b], start[b]+1, ...
+ * (device int32; rows of channel c and kv head h at k + row*k_token + h*k_head + c).  A page whose
+ * first token is among them starts anew; any other keeps its bounds and widens them.  max_new: at
+ * least the largest number of new rows of a sequence (it sizes the launch; more rows than that are
+ * still taken, only slower).  block_table: device int32 [B][max_pages]; the pages of two sequences
+ * that append in one call must differ.  A token past max_pages, or in a page outside [0, npages), is
+ * left out.  NaN elements are skipped.
+ * Errors: TQ_ERR_INVALID_ARG (NULL pointers, bad sizes or dtype), TQ_ERR_UNSUPPORTED (D > 256, B or
+ * Hkv > 65535, a pointer that is not aligned to its element), TQ_ERR_CUDA. */
+int tq_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
+                   const int32_t* start, int B, int Hkv, int D, int64_t max_new, const int32_t* block_table,
+                   int page_tokens, int max_pages, void* bounds, int64_t npages, tq_stream_t stream);
+
+/* tq_sparse_decode_attention -- one decode step over the pages that a score selects: page p of
+ * sequence b scores, for kv head h,
+ *   sum over its query heads and channels of max(q_c lo_c, q_c hi_c)     (sums in 64 bits)
+ * and the `select` pages with the highest scores are attended as by tq_decode_attention, the first
+ * `first` and last `last` pages of the sequence in any case; equal scores go to the lower page, a
+ * NaN score comes last.  A sequence with at most `select` pages attends all of them.
+ * selected (device int32 [B][Hkv][select], may be NULL): the attended pages (logical numbers) in
+ * ascending order, -1 behind the last.  out: device [B][Hq][D] of q_dtype (F32, BF16 or F16).
+ * bounds: as kept by tq_page_bounds (bounds_dtype, bounds_pages pages).  block_table, page_tokens and
+ * channel_perm as in tq_decode_opts; the table is required, the permutation may be NULL.  Other
+ * arguments, supported caches and errors as tq_decode_attention_ex; TQ_ERR_INVALID_ARG too for select < 1,
+ * negative first or last, a NULL table or bounds.  An entry of the table outside the caches reads page
+ * 0 and is reported as device error 901 if the page is attended; outside the bounds it scores last. */
+typedef struct tq_sparse_opts {
+  const void* bounds;
+  int bounds_dtype;
+  int64_t bounds_pages;
+  int select, first, last;
+  int32_t* selected;
+  const int32_t* block_table;
+  int page_tokens;
+  const int32_t* channel_perm;
+} tq_sparse_opts;
+size_t tq_sparse_workspace_size(int B, int Hq, int Hkv, int D, int ngroups, int64_t max_len, int page_tokens, int select);
+int tq_sparse_decode_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, const int* group_off,
+                               int ngroups, const void* q, int q_dtype, const tq_packed* kcache,
+                               const tq_packed* vcache, const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
+                               int64_t max_len, float scale, void* out, const tq_sparse_opts* opts, void* workspace,
+                               size_t ws_bytes, tq_stream_t stream);
+
+/* tq_tree_attention -- attention of drafted tokens that are verified together.  The drafted tokens'
+ * keys and values are in the cache already (tq_quantize_kv): they are the last n_b = draft_lens[b] of
+ * sequence b's seq_lens[b] tokens.  Query row j < n_b of sequence b attends all tokens before the
+ * drafted ones and drafted token i where bit i % 64 of tree_mask[b][j][i / 64] is set (its ancestors and
+ * itself, for a tree; any mask is allowed).  A row that attends nothing, and every row j >= n_b, gives
+ * zeros.  Accepted tokens are kept by quantizing them to their final slots; nothing else in the cache
+ * changes.
+ * q, out: device [B][T][Hq][D] of q_dtype (F32, BF16, F16); 1 <= T <= 256.  draft_lens: device int32 [B],
+ * clamped to [0, min(T, seq_lens[b])], or NULL: T each.  tree_mask: device uint64 [B][T][(T+63)/64], or
+ * NULL: a chain (row j attends the drafted tokens up to j).  The products run on fp16 operands with
+ * 32-bit sums, so an F32 result is good to about 1e-3 as well.  Supported caches, other arguments,
+ * layouts and errors as tq_decode_attention_ex (opts may be NULL); TQ_ERR_UNSUPPORTED for T outside
+ * [1, 256]. */
+size_t tq_tree_workspace_size(int B, int T, int Hq, int Hkv, int D, int ngroups, int64_t max_len);
+int tq_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, const int* group_off, int ngroups,
+                      const void* q, int q_dtype, const tq_packed* kcache, const tq_packed* vcache,
+                      const int32_t* seq_lens, const int32_t* draft_lens, const uint64_t* tree_mask, int B, int T,
+                      int Hq, int Hkv, int D, int64_t max_len, float scale, void* out, const tq_decode_opts* opts,
+                      void* workspace, size_t ws_bytes, tq_stream_t stream);
+
+/* tq_tree_mask -- host: the masks of trees given by parents.  parent (host int32 [B][T]): the drafted
+ * token that token j of sequence b follows, in [-1, j) (-1: the last context token).  mask (host uint64
+ * [B][T][(T+63)/64]): bit i of row j set where i is j or an ancestor of j.
+ * Errors: TQ_ERR_INVALID_ARG (NULL pointers, bad sizes, a parent outside [-1, j)). */
+int tq_tree_mask(const int32_t* parent, int B, int T, uint64_t* mask);
+
 /* Test hooks (not for production use).
  * tq_debug_set_wait_limit -- limit, in nanoseconds, of the pipeline waits of the
  *   dequantize, search and workspace-quantize kernels launched after the call (default 2 s;

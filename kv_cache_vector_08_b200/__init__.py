@@ -17,6 +17,8 @@ __all__ = [
     "MODE_PROD", "MODE_MSE", "TQError", "Context", "Packed", "host_params", "alloc_packed",
     "quantize_kv", "quantize_workspace_size", "channel_perm_by_score", "dequantize", "prepare_queries", "attn_logits", "decode_attention",
     "decode_workspace_size", "search_topk", "launch_count", "lib_path", "lib",
+    "rope", "rope_frequencies", "page_bounds", "alloc_page_bounds", "SparsePlan", "sparse_decode_attention",
+    "sparse_workspace_size", "TreePlan", "tree_attention", "tree_workspace_size", "tree_mask",
 ]
 
 MODE_PROD = 0
@@ -41,6 +43,22 @@ class _Packed(ctypes.Structure):
 
 class _DecodeOpts(ctypes.Structure):
     _fields_ = [("channel_perm", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("page_tokens", ctypes.c_int)]
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int), ("x_token", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64)]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class _SparseOpts(ctypes.Structure):
+    _fields_ = [("bounds", ctypes.c_void_p), ("bounds_dtype", ctypes.c_int), ("bounds_pages", ctypes.c_int64),
+                ("select", ctypes.c_int), ("first", ctypes.c_int), ("last", ctypes.c_int), ("selected", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("page_tokens", ctypes.c_int), ("channel_perm", ctypes.c_void_p)]
 
 
 class _Info(ctypes.Structure):
@@ -86,6 +104,16 @@ def lib():
         "tq_quantize_kv_cols": (I, [P, P, I, I64, I64, P, PK, P, P, SZ, P]),
         "tq_search_workspace_size": (SZ, [P, I64, I64, I]),
         "tq_search_topk": (I, [P, P, I64, PK, I64, I, P, P, P, SZ, P]),
+        "tq_rope": (I, [ctypes.POINTER(_RopeTensor), I, I, I64, I, I, P, P, I, ctypes.c_double, I, P]),
+        "tq_rope_frequencies": (I, [I, ctypes.c_double, ctypes.POINTER(_RopeScaling), P, ctypes.POINTER(ctypes.c_double)]),
+        "tq_page_bounds": (I, [P, I, I64, I64, P, P, I, I, I, I64, P, I, I, P, I64, P]),
+        "tq_sparse_workspace_size": (SZ, [I, I, I, I, I, I64, I, I]),
+        "tq_sparse_decode_attention": (I, [P, P, P, I, P, I, PK, PK, P, I, I, I, I, I64, F, P,
+                                           ctypes.POINTER(_SparseOpts), P, SZ, P]),
+        "tq_tree_workspace_size": (SZ, [I, I, I, I, I, I, I64]),
+        "tq_tree_attention": (I, [P, P, P, I, P, I, PK, PK, P, P, P, I, I, I, I, I, I64, F, P,
+                                  ctypes.POINTER(_DecodeOpts), P, SZ, P]),
+        "tq_tree_mask": (I, [P, I, I, P]),
         "tq_last_error": (ctypes.c_char_p, []),
         "tq_kernel_launch_count": (U64, []),
         "tq_get_device_error": (I, [P, ctypes.POINTER(I)]),
@@ -368,3 +396,233 @@ def search_topk(ctx: Context, q, db: Packed, N: int, k: int, stream=None):
     _check(lib().tq_search_topk(ctx.handle, _ptr(q), nq, ctypes.byref(ps), N, k, _ptr(scores), _ptr(ids),
                                 _ptr(ws), ws.numel(), _stream(stream)))
     return scores, ids
+
+
+# ------------------------------------------------------------------ around the cache
+ROPE_SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+def _on_current_device(*tensors):
+    """Every call launches on the current device: a tensor of another one (or of the host) is refused."""
+    dev = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError("expected CUDA tensors on the current device (cuda:%d), got one on %s" % (dev, t.device))
+
+
+def _int32(t, shape, name):
+    torch = _torch()
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, tuple(shape)))
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling=None, factor: float = 1.0, original_len: float = 0.0,
+                     low: float = 1.0, high: float = 32.0):
+    """(float64 numpy [rot/2] frequencies, factor on the rotated values) of rotary positions; scaling None,
+    "linear", "ntk", "bands" or "yarn" (see tq_rope_frequencies in tq.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % sorted(k for k in ROPE_SCALINGS if k))
+    freq = np.zeros(max(int(rot) // 2, 1))
+    f = ctypes.c_double(0.0)
+    s = _RopeScaling(ROPE_SCALINGS[scaling], factor, original_len, low, high)
+    _check(lib().tq_rope_frequencies(int(rot), base, ctypes.byref(s), freq.ctypes.data_as(ctypes.c_void_p),
+                                     ctypes.byref(f)))
+    return freq, f.value
+
+
+def rope(q, k, positions, freqs, *, interleaved: bool = False, factor: float = 1.0, transpose: bool = False,
+         q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [n, Hq, D] and k [n, Hkv, D] (k may be None) in one launch -> (q_out, k_out).
+    positions int32 / int64 CUDA [n]; freqs float64 CUDA [rot/2]; channels from rot on are copied.  The outputs may
+    be q and k themselves.  transpose=True turns back: the gradient of the call without it."""
+    torch = _torch()
+    D, n = q.shape[-1], q.shape[0]
+    sides = (_RopeTensor * 2)()
+    outs = []
+    given = ((q, q_out),) if k is None else ((q, q_out), (k, k_out))
+    for i, (x, out) in enumerate(given):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if x.dim() != 3 or x.shape[0] != n or x.shape[2] != D or out.shape != x.shape or x.dtype != q.dtype \
+                or out.dtype != q.dtype or x.stride(2) != 1 or out.stride(2) != 1:
+            raise ValueError("q, k and their outputs must be [n, heads, D] of one dtype with unit stride along channels")
+        xs, os_ = x.stride(), out.stride()
+        sides[i] = _RopeTensor(x.data_ptr(), out.data_ptr(), x.shape[1], xs[0], xs[1], os_[0], os_[1])
+        outs.append(out)
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float64 tensor [rot/2]")
+    if positions.dtype not in (torch.int32, torch.int64) or positions.shape != (n,) or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 or int64 tensor [n]")
+    _on_current_device(q, k, positions, freqs, *outs)
+    _check(lib().tq_rope(sides, len(given), _dtype_code(q), n, D, 2 * freqs.shape[0], freqs.data_ptr(),
+                         positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32, factor,
+                         (1 if interleaved else 0) | (2 if transpose else 0), _stream(stream)))
+    return outs[0], (outs[1] if k is not None else None)
+
+
+def alloc_page_bounds(npages: int, Hkv: int, D: int, dtype, device=None):
+    """Bounds of a paged cache's keys, [npages, Hkv, 2, D] (minimum, maximum): kept by page_bounds."""
+    torch = _torch()
+    return torch.zeros((npages, Hkv, 2, D), dtype=dtype, device=device or torch.device("cuda", torch.cuda.current_device()))
+
+
+def page_bounds(k, cu_new, start, block_table, page_tokens: int, bounds, max_new: int, stream=None):
+    """Fold the new keys k [rows, Hkv, D] into the bounds of their pages (in place) -> bounds.  Sequence b appends
+    rows cu_new[b] .. cu_new[b+1]-1 as its tokens start[b], ...; max_new >= the largest number of new rows."""
+    if k.dim() != 3 or k.stride(2) != 1 or bounds.dtype != k.dtype or not bounds.is_contiguous() \
+            or bounds.dim() != 4 or tuple(bounds.shape[1:]) != (k.shape[1], 2, k.shape[2]):
+        raise ValueError("k must be [rows, Hkv, D] with unit stride along channels, bounds contiguous [pages, Hkv, 2, D] of its dtype")
+    B = start.shape[0]
+    _int32(start, (B,), "start")
+    _int32(cu_new, (B + 1,), "cu_new")
+    _int32(block_table, (B, block_table.shape[-1]), "block_table")
+    _on_current_device(k, cu_new, start, block_table, bounds)
+    _check(lib().tq_page_bounds(k.data_ptr(), _dtype_code(k), k.stride(0), k.stride(1), cu_new.data_ptr(), start.data_ptr(),
+                                B, k.shape[1], k.shape[2], int(max_new), block_table.data_ptr(), int(page_tokens),
+                                block_table.shape[1], bounds.data_ptr(), bounds.shape[0], _stream(stream)))
+    return bounds
+
+
+class _CachePlan:
+    """Pre-marshalled caches of the calls below (as DecodePlan keeps them)."""
+
+    def __init__(self, kctx, vctx, group_off, kcache, vcache, B, Hq, Hkv, D, max_len):
+        G = len(kctx)
+        self.G, self.B, self.Hq, self.Hkv, self.D, self.max_len = G, B, Hq, Hkv, D, max_len
+        self._k = (ctypes.c_void_p * G)(*[c.handle.value for c in kctx])
+        self._v = (ctypes.c_void_p * G)(*[c.handle.value for c in vctx])
+        self._off = (ctypes.c_int * (G + 1))(*list(group_off))
+        self._kc = (_Packed * G)(*[p.struct() for p in kcache])
+        self._vc = (_Packed * G)(*[p.struct() for p in vcache])
+        self._keep = (kctx, vctx, kcache, vcache)
+        self.device = kcache[0].codes.device
+
+    def _workspace(self, need):
+        return _torch().empty(max(need, 1), dtype=_torch().uint8, device=self.device)
+
+    def _query(self, q, shape, out):
+        if tuple(q.shape) != shape:
+            raise ValueError("q must be %s, got %s" % (shape, tuple(q.shape)))
+        q = q.contiguous()
+        if out is None:
+            out = _torch().empty(shape, dtype=q.dtype, device=q.device)
+        elif tuple(out.shape) != shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous, with the shape and dtype of q")
+        return q, out
+
+
+def sparse_workspace_size(B, Hq, Hkv, D, ngroups, max_len, page_tokens, select) -> int:
+    return int(lib().tq_sparse_workspace_size(B, Hq, Hkv, D, ngroups, max_len, page_tokens, select))
+
+
+class SparsePlan(_CachePlan):
+    """Caches, block table and workspace of tq_sparse_decode_attention.  Calls that may overlap (on several streams,
+    or captured into several graphs) need a plan each: they share its workspace and its `selected`."""
+
+    def __init__(self, kctx: Sequence[Context], vctx: Sequence[Context], group_off: Sequence[int],
+                 kcache: Sequence[Packed], vcache: Sequence[Packed], B, Hq, Hkv, D, max_len, *, block_table,
+                 page_tokens: int, select: int, first: int = 1, last: int = 1, channel_perm=None):
+        super().__init__(kctx, vctx, group_off, kcache, vcache, B, Hq, Hkv, D, max_len)
+        torch = _torch()
+        if page_tokens <= 0 or max_len % page_tokens != 0:
+            raise ValueError("page_tokens must divide max_len")
+        _int32(block_table, (B, max_len // page_tokens), "block_table")
+        if channel_perm is not None:
+            _int32(channel_perm, (Hkv, D), "channel_perm")
+        self.select = int(select)
+        self.selected = torch.empty((B, Hkv, max(self.select, 1)), dtype=torch.int32, device=self.device)
+        self._opts = _SparseOpts(0, 0, 0, self.select, int(first), int(last), self.selected.data_ptr(),
+                                 block_table.data_ptr(), int(page_tokens),
+                                 0 if channel_perm is None else channel_perm.data_ptr())
+        self._keep_opts = (block_table, channel_perm)
+        self.workspace = self._workspace(sparse_workspace_size(B, Hq, Hkv, D, self.G, max_len, page_tokens, self.select))
+
+    def __call__(self, q, bounds, seq_lens, scale: float, out=None, stream=None):
+        """q [B, Hq, D] -> (out [B, Hq, D] of q's dtype, selected int32 [B, Hkv, select]: the plan's own tensor)."""
+        q, out = self._query(q, (self.B, self.Hq, self.D), out)
+        if bounds.dim() != 4 or tuple(bounds.shape[1:]) != (self.Hkv, 2, self.D) or not bounds.is_contiguous():
+            raise ValueError("bounds must be contiguous [pages, Hkv, 2, D]")
+        _int32(seq_lens, (self.B,), "seq_lens")
+        _on_current_device(q, bounds, seq_lens, out)
+        o = self._opts
+        o.bounds, o.bounds_dtype, o.bounds_pages = bounds.data_ptr(), _dtype_code(bounds), bounds.shape[0]
+        _check(lib().tq_sparse_decode_attention(
+            self._k, self._v, self._off, self.G, q.data_ptr(), _dtype_code(q), self._kc, self._vc, seq_lens.data_ptr(),
+            self.B, self.Hq, self.Hkv, self.D, self.max_len, scale, out.data_ptr(), ctypes.byref(o),
+            self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
+        return out, self.selected
+
+
+def sparse_decode_attention(kctx, vctx, group_off, q, bounds, kcache, vcache, seq_lens, Hkv, max_len, scale, *,
+                            block_table, page_tokens, select, first=1, last=1, out=None, stream=None, channel_perm=None):
+    """One decode step over the pages that their key bounds select -> (out, selected); see tq.h."""
+    B, Hq, D = q.shape
+    plan = SparsePlan(kctx, vctx, group_off, kcache, vcache, B, Hq, Hkv, D, max_len, block_table=block_table,
+                      page_tokens=page_tokens, select=select, first=first, last=last, channel_perm=channel_perm)
+    return plan(q, bounds, seq_lens, scale, out, stream)
+
+
+def tree_workspace_size(B, T, Hq, Hkv, D, ngroups, max_len) -> int:
+    return int(lib().tq_tree_workspace_size(B, T, Hq, Hkv, D, ngroups, max_len))
+
+
+def tree_mask(parents) -> np.ndarray:
+    """Masks of drafted trees: parents int [B, T] (or [T]), each in [-1, j) -> int64 [B, T, ceil(T / 64)] with bit i of
+    row j set where i is j or one of its ancestors (move it to the GPU with torch.from_numpy)."""
+    p = np.ascontiguousarray(parents, dtype=np.int32)
+    p = p[None] if p.ndim == 1 else p
+    if p.ndim != 2:
+        raise ValueError("parents must be [B, T] or [T]")
+    B, T = p.shape
+    m = np.zeros((B, T, (T + 63) // 64), dtype=np.int64)
+    _check(lib().tq_tree_mask(p.ctypes.data_as(ctypes.c_void_p), B, T, m.ctypes.data_as(ctypes.c_void_p)))
+    return m
+
+
+class TreePlan(_CachePlan):
+    """Caches, block table and workspace of tq_tree_attention.  Calls that may overlap (on several streams, or captured
+    into several graphs) need a plan each: they share its workspace."""
+
+    def __init__(self, kctx: Sequence[Context], vctx: Sequence[Context], group_off: Sequence[int],
+                 kcache: Sequence[Packed], vcache: Sequence[Packed], B, T, Hq, Hkv, D, max_len, *, channel_perm=None,
+                 block_table=None, page_tokens: int = 0):
+        super().__init__(kctx, vctx, group_off, kcache, vcache, B, Hq, Hkv, D, max_len)
+        self.T = int(T)
+        if block_table is not None:
+            if page_tokens <= 0 or max_len % page_tokens != 0:
+                raise ValueError("page_tokens must divide max_len")
+            _int32(block_table, (B, max_len // page_tokens), "block_table")
+        if channel_perm is not None:
+            _int32(channel_perm, (Hkv, D), "channel_perm")
+        self._opts = _DecodeOpts(0 if channel_perm is None else channel_perm.data_ptr(),
+                                 0 if block_table is None else block_table.data_ptr(), int(page_tokens))
+        self._keep_opts = (channel_perm, block_table)
+        self.workspace = self._workspace(tree_workspace_size(B, self.T, Hq, Hkv, D, self.G, max_len))
+
+    def __call__(self, q, seq_lens, draft_lens, mask, scale: float, out=None, stream=None):
+        """q [B, T, Hq, D] -> out of its shape and dtype.  draft_lens int32 [B] or None (T each); mask int64
+        [B, T, ceil(T / 64)] (tree_mask) or None (a chain)."""
+        torch = _torch()
+        q, out = self._query(q, (self.B, self.T, self.Hq, self.D), out)
+        _int32(seq_lens, (self.B,), "seq_lens")
+        if draft_lens is not None:
+            _int32(draft_lens, (self.B,), "draft_lens")
+        if mask is not None and (mask.dtype != torch.int64 or not mask.is_contiguous()
+                                 or tuple(mask.shape) != (self.B, self.T, (self.T + 63) // 64)):
+            raise ValueError("mask must be a contiguous int64 tensor [B, T, ceil(T / 64)]")
+        _on_current_device(q, seq_lens, draft_lens, mask, out)
+        _check(lib().tq_tree_attention(
+            self._k, self._v, self._off, self.G, q.data_ptr(), _dtype_code(q), self._kc, self._vc, seq_lens.data_ptr(),
+            _ptr(draft_lens), _ptr(mask), self.B, self.T, self.Hq, self.Hkv, self.D, self.max_len, scale, out.data_ptr(),
+            ctypes.byref(self._opts), self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
+        return out
+
+
+def tree_attention(kctx, vctx, group_off, q, kcache, vcache, seq_lens, Hkv, max_len, scale, draft_lens=None, mask=None,
+                   out=None, stream=None, channel_perm=None, block_table=None, page_tokens=0):
+    """Attention of T drafted tokens per sequence, the last ones of its cache, under a tree mask; q [B, T, Hq, D] -> out
+    of its shape and dtype (see tq.h)."""
+    B, T, Hq, D = q.shape
+    plan = TreePlan(kctx, vctx, group_off, kcache, vcache, B, T, Hq, Hkv, D, max_len, channel_perm=channel_perm,
+                    block_table=block_table, page_tokens=page_tokens)
+    return plan(q, seq_lens, draft_lens, mask, scale, out, stream)

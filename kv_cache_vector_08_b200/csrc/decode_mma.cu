@@ -647,7 +647,7 @@ constexpr int kPrepRows = 16;
 
 struct PrepArgs {
   const void* q;
-  int q_f32;
+  int q_dtype;
   int nrows, D, G, Hq, rep, dg, obs;   // obs: output blocks (16 or 64 outputs) per group
   const int32_t* perm;                 // [Hkv][D] channel permutation or NULL
   int off[2];
@@ -655,6 +655,12 @@ struct PrepArgs {
   const float* stt[2];
   float* qp;                           // [nrows][G][2][D]
 };
+
+__device__ __forceinline__ float load_query(const void* q, int dtype, size_t i) {
+  if (dtype == TQ_DTYPE_F32) return __ldg(static_cast<const float*>(q) + i);
+  if (dtype == TQ_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
+  return __half2float(static_cast<const __half*>(q)[i]);
+}
 
 __global__ void __launch_bounds__(256) decode_prep_kernel(PrepArgs A) {
   __shared__ __align__(16) float ms[128][16];        // [j][o]: M^T[j][16 ob + o]
@@ -679,8 +685,7 @@ __global__ void __launch_bounds__(256) decode_prep_kernel(PrepArgs A) {
       int ch = off + jj;
       if (A.perm) ch = __ldg(A.perm + (size_t)(((r0 + r) % A.Hq) / A.rep) * A.D + off + jj);
       if (ch >= 0 && ch < A.D)   // (the merge kernel reports an out-of-range entry)
-        v = A.q_f32 ? __ldg(static_cast<const float*>(A.q) + row + ch)
-                    : __bfloat162float(static_cast<const __nv_bfloat16*>(A.q)[row + ch]);
+        v = load_query(A.q, A.q_dtype, row + ch);
     }
     xs[r][jj] = v;
   }
@@ -734,8 +739,7 @@ __global__ void __launch_bounds__(256) decode_prep_wide_kernel(PrepArgs A) {
       int ch = off + j;
       if (A.perm) ch = __ldg(A.perm + (size_t)(((r0 + r) % A.Hq) / A.rep) * A.D + off + j);
       if (ch >= 0 && ch < A.D)   // (the merge kernel reports an out-of-range entry)
-        v = A.q_f32 ? __ldg(static_cast<const float*>(A.q) + row + ch)
-                    : __bfloat162float(static_cast<const __nv_bfloat16*>(A.q)[row + ch]);
+        v = load_query(A.q, A.q_dtype, row + ch);
     }
     xs[r][j] = v;
   }
@@ -763,8 +767,10 @@ struct Merge2Args {
   int nsplit, D, G;
   int off[3];
   const float* PiV[2];
-  float* out;
-  const int32_t* perm;   // channel permutation [Hkv][D] (NULL: identity): group channel c -> perm[kv][c]
+  void* out;
+  int out_dtype;
+  const int32_t* perm;   // channel permutation [perm_heads][D] (NULL: identity): group channel c -> perm[kv][c]
+  int perm_heads;        // kv heads of the permutation; CTAs go through them in turn
   int Hq, rep, Hkv, nsub;
   int pi_floats;         // floats of the staged rotations (a multiple of 4)
   int stage_parts;       // copy the CTA's split partials into shared memory first (they fit)
@@ -886,14 +892,19 @@ __global__ void __launch_bounds__(kMergeHThreads, 4) decode_merge_heads_kernel(M
 #pragma unroll
       for (int hh = 0; hh < kRep; ++hh) o[hh] = fmaf(pv, s_v[hh][goff + i], o[hh]);
     }
-    const int oc_ch = A.perm ? A.perm[(size_t)hk * D + c] : c;
+    const int oc_ch = A.perm ? A.perm[(size_t)(bh % A.perm_heads) * D + c] : c;
     if (oc_ch < 0 || oc_ch >= D) {
       if (A.err) atomicCAS(A.err, 0, (int)kErrPermRange);
       continue;
     }
 #pragma unroll
     for (int hh = 0; hh < kRep; ++hh)
-      if (hh < nh) A.out[(size_t)(row0 + hh) * D + oc_ch] = o[hh];
+      if (hh < nh) {
+        const size_t at = (size_t)(row0 + hh) * D + oc_ch;
+        if (A.out_dtype == TQ_DTYPE_F32) static_cast<float*>(A.out)[at] = o[hh];
+        else if (A.out_dtype == TQ_DTYPE_BF16) static_cast<__nv_bfloat16*>(A.out)[at] = __float2bfloat16_rn(o[hh]);
+        else static_cast<__half*>(A.out)[at] = __float2half_rn(o[hh]);
+      }
   }
 }
 
@@ -901,7 +912,7 @@ __global__ void __launch_bounds__(kMergeHThreads, 4) decode_merge_heads_kernel(M
 int launch_prep(const void* q, int q_dtype, int nrows, const tq_ctx* const* kctx, const int* off, int G, float* qp,
                 int D, const int32_t* perm, int Hq, int rep, cudaStream_t st) {
   PrepArgs P{};
-  P.q = q; P.q_f32 = q_dtype == TQ_DTYPE_F32; P.nrows = nrows; P.D = D; P.G = G; P.Hq = Hq; P.rep = rep;
+  P.q = q; P.q_dtype = q_dtype; P.nrows = nrows; P.D = D; P.G = G; P.Hq = Hq; P.rep = rep;
   P.dg = kctx[0]->lay.d; P.obs = P.dg / 16; P.perm = perm; P.qp = qp;
   for (int g = 0; g < G; ++g) { P.off[g] = off[g]; P.pit[g] = kctx[g]->PiT; P.stt[g] = kctx[g]->ST; }
   if (nrows > 256) {
@@ -1146,11 +1157,27 @@ float mmaops::host_luts(const tq_ctx* kc, const tq_ctx* vc, Luts* t) {
   return sc > 0.f ? 1.f / sc : 0.f;
 }
 
+// Whether the caches are ones that the decode kernels are built for.
+bool decode_caches_supported(const tq_ctx* const* kctx, const tq_ctx* const* vctx, int G, const tq_packed* kc,
+                             const tq_packed* vc) {
+  if (G < 1 || G > 2) return false;
+  int sig[2] = {0, 0};
+  for (int g = 0; g < G; ++g) sig[g] = kctx[g]->lay.d * 100 + kctx[g]->lay.planes * 10 + vctx[g]->lay.planes;
+  auto is = [&](int a, int b) { return sig[0] == a && sig[1] == b; };
+  if (!is(12844, 0) && !is(12833, 0) && !is(6444, 6433) && !is(6433, 6422)) return false;
+  // every staged array is read by bulk copies, which need 16-byte aligned sources
+  auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  for (int g = 0; g < G; ++g)
+    if (!a16(kc[g].codes) || !a16(vc[g].codes) || !a16(kc[g].norm) || !a16(kc[g].rnorm) || !a16(vc[g].norm))
+      return false;
+  return true;
+}
+
 // Returns kNotHandled when the shape is outside this kernel's instantiations.
 int launch_decode_mma(const tq_ctx* const* kctx, const tq_ctx* const* vctx, const int* off, int G,
                       const int32_t* perm, const int32_t* table, int page, const void* q, int q_dtype,
                       const tq_packed* kc, const tq_packed* vc, const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
-                      int64_t max_len, float scale, float* out, void* ws, cudaStream_t st) {
+                      int64_t max_len, float scale, void* out, void* ws, cudaStream_t st, const DecodeView& view) {
   if (G > 2 || D > 256) return kNotHandled;
   int sig[2] = {0, 0};
   for (int g = 0; g < G; ++g) {
@@ -1164,13 +1191,7 @@ int launch_decode_mma(const tq_ctx* const* kctx, const tq_ctx* const* vctx, cons
   using C64_44 = GroupCfg<64, 4, 4>;
   using C64_33 = GroupCfg<64, 3, 3>;
   using C64_22 = GroupCfg<64, 2, 2>;
-  const bool ok = (G == 1 && (sig[0] == 12844 || sig[0] == 12833)) || is(6444, 6433) || is(6433, 6422);
-  if (!ok) return kNotHandled;
-  // every staged array is read by bulk copies, which need 16-byte aligned sources
-  auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  for (int g = 0; g < G; ++g)
-    if (!a16(kc[g].codes) || !a16(vc[g].codes) || !a16(kc[g].norm) || !a16(kc[g].rnorm) || !a16(vc[g].norm))
-      return kNotHandled;
+  if (!decode_caches_supported(kctx, vctx, G, kc, vc)) return kNotHandled;
 
   const DecodeWs W = decode_ws(B, Hq, Hkv, D, G, max_len);
   if (W.nsplit > kMergeMaxSplit) return kNotHandled;
@@ -1178,7 +1199,7 @@ int launch_decode_mma(const tq_ctx* const* kctx, const tq_ctx* const* vctx, cons
   float* qp = reinterpret_cast<float*>(base + W.qp);
   float* part = reinterpret_cast<float*>(base + W.part);
   {   // every group of an instantiated kernel has the same width (64 or 128)
-    int r = launch_prep(q, q_dtype, B * Hq, kctx, off, G, qp, D, perm, Hq, Hq / Hkv, st);
+    int r = launch_prep(q, q_dtype, B * Hq, kctx, off, G, qp, D, perm, view.perm_Hq ? view.perm_Hq : Hq, Hq / Hkv, st);
     if (r != TQ_OK) return r;
   }
   MmaArgs A{};
@@ -1218,7 +1239,8 @@ int launch_decode_mma(const tq_ctx* const* kctx, const tq_ctx* const* vctx, cons
   if (r != TQ_OK) return r;
   Merge2Args M{};
   M.part = part; M.part_ld = W.part_ld; M.nsplit = W.nsplit; M.D = D; M.G = G; M.out = out; M.err = A.err;
-  M.perm = perm; M.Hq = Hq; M.rep = Hq / Hkv;
+  M.perm = perm; M.perm_heads = view.perm_Hkv ? view.perm_Hkv : Hkv; M.out_dtype = view.out_dtype;
+  M.Hq = Hq; M.rep = Hq / Hkv;
   for (int g = 0; g < G; ++g) { M.off[g] = off[g]; M.PiV[g] = vctx[g]->Pi; }
   M.off[G] = D;
   M.Hkv = Hkv;

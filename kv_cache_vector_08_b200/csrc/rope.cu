@@ -1,0 +1,250 @@
+// Rotary positions of queries and keys, ahead of tq_quantize_kv and the attention calls.
+//
+// Pair i of a head turns by the angle a = pos * freq_i:
+//   y1 = f (x1 cos a - x2 sin a),   y2 = f (x2 cos a + x1 sin a)
+// with (x1, x2) = (x[i], x[i + rot/2]) or, interleaved, (x[2i], x[2i+1]); channels from rot
+// on are copied.  The transposed rotation (the gradient, and for f = 1 the inverse) turns by -a.
+//
+// The angle is formed in 64 bits as a number of turns, pos * (freq / 2 pi), of which only the
+// fraction is kept: positions of 2^31 still give the angle to 2e-7, where a 32-bit product
+// would be off by whole turns.  Its sine and cosine are taken once per token and pair of a
+// block, in shared memory, and serve all heads of both tensors.
+//
+// Bound: HBM (every element is read and written once).  A thread moves one vector of each
+// half of the pairs (half layout) or one vector of pairs (interleaved) at a time; queries and
+// keys go in one launch, since for a decode step the launch is the cost.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int64_t kRopeMaxRow = 1 << 19;   // elements of one token over both tensors
+
+// n / d for n d < 2^40, n < 2^20 by one multiplication
+struct Div {
+  uint64_t m;
+  int d;
+  Div(int d_ = 1) : m(((1ull << 40) + d_ - 1) / d_), d(d_) {}
+  __device__ __forceinline__ int quot(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> 40); }
+};
+
+struct RopeSide {
+  const void* x;
+  void* out;
+  int64_t xt, xh, ot, oh;   // strides in elements: token, head
+};
+
+struct RopeArgs {
+  RopeSide s[2];
+  int heads0;               // heads of the first tensor
+  int64_t n;
+  int rot, D;
+  int tb;                   // tokens per block
+  int per_block;            // units of a block (tb * heads * units)
+  int chunk;                // units per grid.y slice
+  Div per_tok, per_head;    // units of a token, units of a head
+  int rot_units;            // units of a head that rotate (the others copy)
+  const double* freq;
+  const void* pos;
+  int pos64;
+  float factor, sign;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs A) {
+  extern __shared__ float2 s_cs[];   // [tb][rot / 2] (cos, sin), times the factor
+  const int64_t t0 = (int64_t)blockIdx.x * A.tb;
+  const int ntok = (int)(A.n - t0 < A.tb ? A.n - t0 : A.tb), np = A.rot / 2;
+  for (int e = threadIdx.x; e < ntok * np; e += kRopeThreads) {
+    const int t = e / np, i = e - t * np;
+    const double pos = A.pos64 ? (double)static_cast<const int64_t*>(A.pos)[t0 + t]
+                               : (double)static_cast<const int32_t*>(A.pos)[t0 + t];
+    const double turns = pos * (A.freq[i] * 0.15915494309189533577);
+    float si, co;
+    sincospif((float)(2.0 * (turns - rint(turns))), &si, &co);
+    s_cs[e] = make_float2(co * A.factor, si * A.factor * A.sign);
+  }
+  __syncthreads();
+  const int u0 = blockIdx.y * A.chunk, u1 = min(u0 + A.chunk, ntok * A.per_tok.d);
+  using VT = Vec<T, V>;
+#pragma unroll 4
+  for (int u = u0 + threadIdx.x; u < u1; u += kRopeThreads) {
+    const int t = A.per_tok.quot(u), r = u - t * A.per_tok.d;
+    int h = A.per_head.quot(r);
+    const int k = r - h * A.per_head.d;
+    const bool second = h >= A.heads0;
+    h -= second ? A.heads0 : 0;
+    // (selected field by field: an indexed parameter struct would be copied to local memory)
+    const T* x = static_cast<const T*>(second ? A.s[1].x : A.s[0].x) +
+                 (t0 + t) * (second ? A.s[1].xt : A.s[0].xt) + h * (second ? A.s[1].xh : A.s[0].xh);
+    T* o = static_cast<T*>(second ? A.s[1].out : A.s[0].out) +
+           (t0 + t) * (second ? A.s[1].ot : A.s[0].ot) + h * (second ? A.s[1].oh : A.s[0].oh);
+    if (k >= A.rot_units) {
+      const int c = A.rot + (k - A.rot_units) * V;
+      *reinterpret_cast<VT*>(o + c) = *reinterpret_cast<const VT*>(x + c);
+      continue;
+    }
+    const float2* cs = s_cs + t * np;
+    if constexpr (INTER && V > 1) {
+      VT a = *reinterpret_cast<const VT*>(x + k * V);
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 w = cs[k * (V / 2) + j];
+        const float x1 = to_f<T>(a.v[2 * j]), x2 = to_f<T>(a.v[2 * j + 1]);
+        a.v[2 * j] = from_f<T>(x1 * w.x - x2 * w.y);
+        a.v[2 * j + 1] = from_f<T>(x2 * w.x + x1 * w.y);
+      }
+      *reinterpret_cast<VT*>(o + k * V) = a;
+    } else {
+      // V pairs: vectors of both halves, or (interleaved without alignment) one pair
+      const int i1 = INTER ? 2 * k : k * V, i2 = INTER ? 2 * k + 1 : k * V + np;
+      VT a = *reinterpret_cast<const VT*>(x + i1), b = *reinterpret_cast<const VT*>(x + i2);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float2 w = cs[k * V + j];
+        const float x1 = to_f<T>(a.v[j]), x2 = to_f<T>(b.v[j]);
+        a.v[j] = from_f<T>(x1 * w.x - x2 * w.y);
+        b.v[j] = from_f<T>(x2 * w.x + x1 * w.y);
+      }
+      *reinterpret_cast<VT*>(o + i1) = a;
+      *reinterpret_cast<VT*>(o + i2) = b;
+    }
+  }
+}
+
+template <typename T, int V>
+int launch_v(RopeArgs A, int heads, bool inter, int sms, cudaStream_t st) {
+  A.rot_units = inter ? (V > 1 ? A.rot / V : A.rot / 2) : A.rot / 2 / V;
+  const int per_head = A.rot_units + (A.D - A.rot) / V;
+  A.per_head = Div(per_head);
+  A.per_tok = Div(per_head * heads);
+  // A block takes about four units a thread: whole tokens (their sines are shared by the
+  // heads), or, when the tokens are too few for the device, slices of one token's heads.
+  const int want = 4 * kRopeThreads;
+  int64_t tb = std::max<int64_t>(1, want / A.per_tok.d);
+  tb = std::max<int64_t>(1, std::min<int64_t>(tb, A.n / (2 * sms)));
+  tb = std::min<int64_t>(tb, std::max(1, 24 * 1024 / std::max(1, A.rot / 2 * (int)sizeof(float2))));
+  A.tb = (int)tb;
+  A.per_block = A.tb * A.per_tok.d;
+  const int64_t blocks = (A.n + tb - 1) / tb;
+  int slices = 1;
+  if (blocks < 2 * sms) slices = (int)std::min<int64_t>((2 * sms + blocks - 1) / blocks, (A.per_block + kRopeThreads - 1) / kRopeThreads);
+  A.chunk = (A.per_block + slices - 1) / slices;
+  slices = (A.per_block + A.chunk - 1) / A.chunk;
+  const dim3 grid((unsigned)blocks, (unsigned)slices);
+  const size_t sm = (size_t)A.tb * (A.rot / 2) * sizeof(float2);
+  if (inter) rope_kernel<T, V, true><<<grid, kRopeThreads, sm, st>>>(A);
+  else rope_kernel<T, V, false><<<grid, kRopeThreads, sm, st>>>(A);
+  count_launch();
+  return check_launch("rope_kernel");
+}
+
+template <typename T>
+int launch_t(const RopeArgs& A, int heads, bool inter, int vec, int sms, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2)
+    if (vec >= 8) return launch_v<T, 8>(A, heads, inter, sms, st);
+  if (vec >= 4) return launch_v<T, 4>(A, heads, inter, sms, st);
+  if (vec >= 2) return launch_v<T, 2>(A, heads, inter, sms, st);
+  return launch_v<T, 1>(A, heads, inter, sms, st);
+}
+
+}  // namespace
+
+int launch_rope(const tq_rope_tensor* t, int nt, int dtype, int64_t n, int D, int rot, const double* freq,
+                const void* pos, int pos_bits, double factor, int flags, cudaStream_t st) {
+  const int es = dtype == TQ_DTYPE_F32 ? 4 : 2;
+  const bool inter = (flags & TQ_ROPE_INTERLEAVED) != 0;
+  RopeArgs A{};
+  int heads = 0;
+  // widest vector that divides the rotating halves (or pairs) and the copied rest, and that
+  // every pointer and stride is aligned to
+  int vec = 16 / es;
+  auto fit = [&](int64_t elems) { while (vec > 1 && elems % vec != 0) vec /= 2; };
+  auto fit_ptr = [&](const void* p) { while (vec > 1 && reinterpret_cast<uintptr_t>(p) % ((size_t)vec * es) != 0) vec /= 2; };
+  fit(inter ? rot : rot / 2);
+  fit(D - rot);
+  fit(rot);
+  int at = 0;
+  for (int i = 0; i < nt; ++i) {
+    if (t[i].heads == 0) continue;
+    RopeSide& s = A.s[at++];
+    s = RopeSide{t[i].x, t[i].out, t[i].x_token, t[i].x_head, t[i].out_token, t[i].out_head};
+    if (at == 1) A.heads0 = t[i].heads;
+    heads += t[i].heads;
+    fit_ptr(s.x);
+    fit_ptr(s.out);
+    for (int64_t v : {s.xt, s.ot}) if (n > 1) fit(v);
+    for (int64_t v : {s.xh, s.oh}) if (t[i].heads > 1) fit(v);
+  }
+  if (at == 0) return TQ_OK;
+  if ((int64_t)heads * D > kRopeMaxRow)
+    return fail(TQ_ERR_UNSUPPORTED, "tq_rope: one token has more than 2^19 elements");
+  A.n = n; A.rot = rot; A.D = D; A.freq = freq; A.pos = pos; A.pos64 = pos_bits == 64;
+  A.factor = (float)factor;
+  A.sign = (flags & TQ_ROPE_TRANSPOSE) ? -1.f : 1.f;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "tq_rope: device query");
+  if (dtype == TQ_DTYPE_F32) return launch_t<float>(A, heads, inter, vec, sms, st);
+  if (dtype == TQ_DTYPE_BF16) return launch_t<__nv_bfloat16>(A, heads, inter, vec, sms, st);
+  return launch_t<__half>(A, heads, inter, vec, sms, st);
+}
+
+// Frequencies of the usual long-context rules (host, 64 bits).
+int rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* freq, double* factor) {
+  const int np = rot / 2;
+  const double two_pi = 2.0 * M_PI;
+  const int kind = s ? s->kind : TQ_ROPE_SCALE_NONE;
+  if (kind == TQ_ROPE_SCALE_NTK) base *= std::pow(s->factor, rot > 2 ? (double)rot / (rot - 2) : 1.0);
+  for (int i = 0; i < np; ++i) freq[i] = std::pow(base, -2.0 * i / rot);
+  *factor = 1.0;
+  if (kind == TQ_ROPE_SCALE_LINEAR) {
+    for (int i = 0; i < np; ++i) freq[i] /= s->factor;
+  } else if (kind == TQ_ROPE_SCALE_BANDS) {
+    for (int i = 0; i < np; ++i) {
+      const double turns = s->original_len * freq[i] / two_pi;
+      const double w = std::min(1.0, std::max(0.0, (turns - s->low) / (s->high - s->low)));
+      freq[i] *= w + (1.0 - w) / s->factor;
+    }
+  } else if (kind == TQ_ROPE_SCALE_YARN) {
+    // pair index at which a frequency makes `turns` turns over the original length
+    auto pair = [&](double turns) { return rot * std::log(s->original_len / (turns * two_pi)) / (2.0 * std::log(base)); };
+    const double lo = std::max(std::floor(pair(s->high)), 0.0), hi = std::min(std::ceil(pair(s->low)), rot - 1.0);
+    for (int i = 0; i < np; ++i) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+      freq[i] = freq[i] / s->factor * ramp + freq[i] * (1.0 - ramp);
+    }
+    *factor = s->factor > 1.0 ? 0.1 * std::log(s->factor) + 1.0 : 1.0;
+  }
+  return TQ_OK;
+}
+
+}  // namespace tq

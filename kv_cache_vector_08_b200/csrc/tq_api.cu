@@ -71,6 +71,9 @@ int check_device(const tq_ctx* ctx) {
   return TQ_OK;
 }
 
+bool bad_dtype(int t) { return t != TQ_DTYPE_F32 && t != TQ_DTYPE_BF16 && t != TQ_DTYPE_F16; }
+size_t elem_size(int t) { return t == TQ_DTYPE_F32 ? 4 : 2; }
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_packed(const tq_ctx* ctx, const tq_packed* pk, const char* name) {
@@ -207,13 +210,14 @@ int check_args_common(int d, int bits, int mode) {
 // tq_decode_attention_static, which checks its own scratch size after these).
 int check_decode_args(const tq_ctx* const* kctx, const tq_ctx* const* vctx, const int* group_off, int ngroups,
                       const void* q, int q_dtype, const tq_packed* kcache, const tq_packed* vcache,
-                      const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int64_t max_len, const float* out,
-                      int page) {
+                      const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int64_t max_len, const void* out,
+                      int page, bool any_dtype) {
   if (!kctx || !vctx || !group_off || !kcache || !vcache) return fail(TQ_ERR_INVALID_ARG, "NULL argument");
   if (ngroups < 1 || ngroups > 4) return fail(TQ_ERR_UNSUPPORTED, "ngroups must be in [1, 4]");
   if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_len < 0) return fail(TQ_ERR_INVALID_ARG, "bad sizes");
   if (Hq % Hkv != 0) return fail(TQ_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
-  if (q_dtype != TQ_DTYPE_F32 && q_dtype != TQ_DTYPE_BF16) return fail(TQ_ERR_INVALID_ARG, "q_dtype must be F32 or BF16");
+  if (any_dtype ? bad_dtype(q_dtype) : q_dtype != TQ_DTYPE_F32 && q_dtype != TQ_DTYPE_BF16)
+    return fail(TQ_ERR_INVALID_ARG, any_dtype ? "q_dtype must be F32, BF16 or F16" : "q_dtype must be F32 or BF16");
   if (group_off[0] != 0 || group_off[ngroups] != D) return fail(TQ_ERR_INVALID_ARG, "group_off must span [0, D]");
   if (B == 0) return TQ_OK;
   if (!q || !seq_lens || !out) return fail(TQ_ERR_INVALID_ARG, "NULL q, seq_lens or out");
@@ -569,6 +573,182 @@ int tq_search_topk(const tq_ctx* ctx, const float* q, int64_t nq, const tq_packe
   if (!workspace || ws_bytes < need) return fail(TQ_ERR_WORKSPACE, "workspace too small");
   if ((r = check_device(ctx)) != TQ_OK) return r;
   return launch_search(ctx, q, nq, db, N, k, scores, ids, workspace, (cudaStream_t)stream);
+}
+
+int tq_rope(const tq_rope_tensor* tensors, int ntensors, int dtype, int64_t n, int D, int rot, const double* freq,
+            const void* pos, int pos_bits, double factor, int flags, tq_stream_t stream) {
+  Range range_("tq_rope");
+  if (!tensors || ntensors < 1 || ntensors > 2) return fail(TQ_ERR_INVALID_ARG, "tq_rope: one or two tensors");
+  if (bad_dtype(dtype)) return fail(TQ_ERR_INVALID_ARG, "tq_rope: dtype must be F32, BF16 or F16");
+  if (n < 0 || D <= 0) return fail(TQ_ERR_INVALID_ARG, "tq_rope: bad sizes");
+  if (rot < 2 || rot > D || rot % 2 != 0) return fail(TQ_ERR_INVALID_ARG, "tq_rope: rot must be even and in [2, D]");
+  if (D > 4096) return fail(TQ_ERR_UNSUPPORTED, "tq_rope: D must be at most 4096");
+  if (pos_bits != 32 && pos_bits != 64) return fail(TQ_ERR_INVALID_ARG, "tq_rope: pos_bits must be 32 or 64");
+  if (flags & ~(TQ_ROPE_INTERLEAVED | TQ_ROPE_TRANSPOSE)) return fail(TQ_ERR_INVALID_ARG, "tq_rope: unknown flags");
+  for (int i = 0; i < ntensors; ++i) {
+    if (tensors[i].heads < 0) return fail(TQ_ERR_INVALID_ARG, "tq_rope: negative head count");
+    if (n == 0 || tensors[i].heads == 0) continue;
+    if (!tensors[i].x || !tensors[i].out) return fail(TQ_ERR_INVALID_ARG, "tq_rope: NULL tensor");
+    if (!aligned(tensors[i].x, elem_size(dtype)) || !aligned(tensors[i].out, elem_size(dtype)))
+      return fail(TQ_ERR_UNSUPPORTED, "tq_rope: a tensor is not aligned to its element");
+  }
+  if (n == 0) return TQ_OK;
+  if (!freq || !pos) return fail(TQ_ERR_INVALID_ARG, "tq_rope: NULL freq or pos");
+  return launch_rope(tensors, ntensors, dtype, n, D, rot, freq, pos, pos_bits, factor, flags, (cudaStream_t)stream);
+}
+
+int tq_rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* freq, double* factor_out) {
+  if (!freq || !factor_out) return fail(TQ_ERR_INVALID_ARG, "tq_rope_frequencies: NULL output");
+  if (rot < 2 || rot % 2 != 0 || !(base > 1.0)) return fail(TQ_ERR_INVALID_ARG, "tq_rope_frequencies: rot must be even, base above 1");
+  if (s) {
+    if (s->kind < TQ_ROPE_SCALE_NONE || s->kind > TQ_ROPE_SCALE_YARN)
+      return fail(TQ_ERR_INVALID_ARG, "tq_rope_frequencies: unknown scaling");
+    if (s->kind != TQ_ROPE_SCALE_NONE && !(s->factor > 0.0))
+      return fail(TQ_ERR_INVALID_ARG, "tq_rope_frequencies: factor must be positive");
+    if ((s->kind == TQ_ROPE_SCALE_BANDS || s->kind == TQ_ROPE_SCALE_YARN) &&
+        (!(s->original_len > 0.0) || !(s->low < s->high) || !(s->low > 0.0)))
+      return fail(TQ_ERR_INVALID_ARG, "tq_rope_frequencies: needs original_len > 0 and 0 < low < high");
+  }
+  return rope_frequencies(rot, base, s, freq, factor_out);
+}
+
+int tq_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
+                   const int32_t* start, int B, int Hkv, int D, int64_t max_new, const int32_t* block_table,
+                   int page_tokens, int max_pages, void* bounds, int64_t npages, tq_stream_t stream) {
+  Range range_("tq_page_bounds");
+  if (bad_dtype(dtype)) return fail(TQ_ERR_INVALID_ARG, "tq_page_bounds: dtype must be F32, BF16 or F16");
+  if (B < 0 || Hkv <= 0 || D <= 0 || max_new < 0 || page_tokens <= 0 || max_pages < 0 || npages < 0)
+    return fail(TQ_ERR_INVALID_ARG, "tq_page_bounds: bad sizes");
+  if (D > 256 || B > 65535 || Hkv > 65535)
+    return fail(TQ_ERR_UNSUPPORTED, "tq_page_bounds: D must be at most 256, B and Hkv at most 65535");
+  if (B == 0 || max_new == 0 || max_pages == 0 || npages == 0) return TQ_OK;
+  if (!k || !cu_new || !start || !block_table || !bounds) return fail(TQ_ERR_INVALID_ARG, "tq_page_bounds: NULL argument");
+  if (!aligned(k, elem_size(dtype)) || !aligned(bounds, elem_size(dtype)))
+    return fail(TQ_ERR_UNSUPPORTED, "tq_page_bounds: a pointer is not aligned to its element");
+  return launch_page_bounds(k, dtype, k_token, k_head, cu_new, start, B, Hkv, D, max_new, block_table, page_tokens,
+                            max_pages, bounds, npages, (cudaStream_t)stream);
+}
+
+// Limits that the sparse and tree calls share with the decode launches.
+static int check_cache_shape(int64_t pairs, int64_t rows, int64_t max_len, const char* what) {
+  if (max_len > (int64_t)1 << 30) return fail(TQ_ERR_UNSUPPORTED, std::string(what) + ": max_len above 2^30");
+  if (pairs > 65535 || rows > (int64_t)1 << 24)
+    return fail(TQ_ERR_UNSUPPORTED, std::string(what) + ": more than 65535 (sequence, kv head, 4 query heads) blocks or "
+                                                        "2^24 query rows");
+  return TQ_OK;
+}
+
+static int unsupported_caches(const char* what) {
+  return fail(TQ_ERR_UNSUPPORTED,
+              std::string(what) + ": supported channel groups are one group of d = 128 with 4 + 4 or 3 + 3 key / value "
+                                  "bits, or two groups of d = 64 with (4 + 4, 3 + 3) or (3 + 3, 2 + 2) bits; caches and "
+                                  "norms 16-byte aligned");
+}
+
+size_t tq_sparse_workspace_size(int B, int Hq, int Hkv, int D, int ngroups, int64_t max_len, int page_tokens,
+                                int select) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || ngroups <= 0 || max_len < 0 || page_tokens <= 0 ||
+      select < 1 || max_len > (int64_t)1 << 30 || (int64_t)select * page_tokens > (int64_t)1 << 30)
+    return 0;
+  return sparse_ws(B, Hq, Hkv, D, ngroups, page_tokens, (int)(max_len / page_tokens), select).total;
+}
+
+int tq_sparse_decode_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, const int* group_off, int ngroups,
+                               const void* q, int q_dtype, const tq_packed* kcache, const tq_packed* vcache,
+                               const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int64_t max_len, float scale,
+                               void* out, const tq_sparse_opts* opts, void* workspace, size_t ws_bytes,
+                               tq_stream_t stream) {
+  Range range_("tq_sparse_decode_attention");
+  if (!opts) return fail(TQ_ERR_INVALID_ARG, "opts is NULL");
+  const int page = opts->page_tokens;
+  if (!opts->block_table || !opts->bounds) return fail(TQ_ERR_INVALID_ARG, "NULL block table or bounds");
+  if (page <= 0 || page % 64 != 0 || max_len < 0 || max_len % page != 0)
+    return fail(TQ_ERR_INVALID_ARG, "page_tokens must be a positive multiple of 64 that divides max_len");
+  if (bad_dtype(opts->bounds_dtype) || opts->bounds_pages < 0) return fail(TQ_ERR_INVALID_ARG, "bad bounds");
+  if (opts->select < 1 || opts->first < 0 || opts->last < 0)
+    return fail(TQ_ERR_INVALID_ARG, "select must be at least 1, first and last not negative");
+  if ((int64_t)opts->select * page > (int64_t)1 << 30) return fail(TQ_ERR_UNSUPPORTED, "select * page_tokens above 2^30");
+  int r = check_decode_args(kctx, vctx, group_off, ngroups, q, q_dtype, kcache, vcache, seq_lens, B, Hq, Hkv, D,
+                            max_len, out, page, true);
+  if (r != TQ_OK) return r;
+  if (B == 0) return TQ_OK;
+  if ((r = check_cache_shape((int64_t)B * Hkv * ((Hq / Hkv + 3) / 4), (int64_t)B * Hq, max_len, "tq_sparse_decode_attention")) != TQ_OK) return r;
+  if (!aligned(opts->bounds, elem_size(opts->bounds_dtype)) || !aligned(out, elem_size(q_dtype)) || !aligned(q, elem_size(q_dtype)))
+    return fail(TQ_ERR_UNSUPPORTED, "q, out or bounds not aligned to its element");
+  if (!decode_caches_supported(kctx, vctx, ngroups, kcache, vcache)) return unsupported_caches("tq_sparse_decode_attention");
+  const SparseWs W = sparse_ws(B, Hq, Hkv, D, ngroups, page, (int)(max_len / page), opts->select);
+  if (!workspace || ws_bytes < W.total) return fail(TQ_ERR_WORKSPACE, "workspace too small");
+  if (!aligned(workspace, 16)) return fail(TQ_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  int64_t pool = INT64_MAX;
+  for (int g = 0; g < ngroups; ++g) pool = std::min(pool, std::min(kcache[g].cap, vcache[g].cap));
+  pool /= (int64_t)Hkv * page;
+  if (pool * Hkv > INT32_MAX) return fail(TQ_ERR_UNSUPPORTED, "more than 2^31 - 1 (page, kv head) pairs");
+  if ((r = launch_page_select(q, q_dtype, seq_lens, B, Hq, Hkv, D, max_len, pool, opts, workspace, W,
+                              (cudaStream_t)stream)) != TQ_OK)
+    return r;
+  char* base = static_cast<char*>(workspace);
+  DecodeView view;
+  view.out_dtype = q_dtype;
+  view.perm_Hq = Hq;
+  view.perm_Hkv = Hkv;
+  r = launch_decode_mma(kctx, vctx, group_off, ngroups, opts->channel_perm,
+                        reinterpret_cast<const int32_t*>(base + W.vtable), page, q, q_dtype, kcache, vcache,
+                        reinterpret_cast<const int32_t*>(base + W.vlen), B * Hkv, Hq / Hkv, 1, D,
+                        (int64_t)opts->select * page, scale, out, base + W.decode, (cudaStream_t)stream, view);
+  return r == kNotHandled ? fail(TQ_ERR_UNSUPPORTED, "tq_sparse_decode_attention: at most 512 context splits") : r;
+}
+
+size_t tq_tree_workspace_size(int B, int T, int Hq, int Hkv, int D, int ngroups, int64_t max_len) {
+  if (B < 0 || T < 1 || T > 256 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D != 128 || ngroups <= 0 || max_len < 0 ||
+      max_len > (int64_t)1 << 30)
+    return 0;
+  return tree_workspace_bytes(B, T, Hq, Hkv, max_len);
+}
+
+int tq_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, const int* group_off, int ngroups,
+                      const void* q, int q_dtype, const tq_packed* kcache, const tq_packed* vcache,
+                      const int32_t* seq_lens, const int32_t* draft_lens, const uint64_t* tree_mask, int B, int T,
+                      int Hq, int Hkv, int D, int64_t max_len, float scale, void* out, const tq_decode_opts* opts,
+                      void* workspace, size_t ws_bytes, tq_stream_t stream) {
+  Range range_("tq_tree_attention");
+  const int32_t* perm = opts ? opts->channel_perm : nullptr;
+  const int32_t* table = opts ? opts->block_table : nullptr;
+  const int page = table ? opts->page_tokens : 0;
+  if (table && (page <= 0 || page % 64 != 0 || max_len % page != 0))
+    return fail(TQ_ERR_INVALID_ARG, "page_tokens must be a positive multiple of 64 that divides max_len");
+  if (T < 1 || T > 256) return fail(TQ_ERR_UNSUPPORTED, "T must be in [1, 256]");
+  int r = check_decode_args(kctx, vctx, group_off, ngroups, q, q_dtype, kcache, vcache, seq_lens, B, Hq, Hkv, D,
+                            max_len, out, page, true);
+  if (r != TQ_OK) return r;
+  if (B == 0) return TQ_OK;
+  if ((r = check_cache_shape((int64_t)B * Hkv * ((Hq / Hkv + 3) / 4), (int64_t)B * T * Hq, max_len, "tq_tree_attention")) != TQ_OK) return r;
+  if (!aligned(out, elem_size(q_dtype)) || !aligned(q, elem_size(q_dtype)))
+    return fail(TQ_ERR_UNSUPPORTED, "q or out not aligned to its element");
+  if (!decode_caches_supported(kctx, vctx, ngroups, kcache, vcache)) return unsupported_caches("tq_tree_attention");
+  const size_t need = tree_workspace_bytes(B, T, Hq, Hkv, max_len);
+  if (!workspace || ws_bytes < need) return fail(TQ_ERR_WORKSPACE, "workspace too small");
+  if (!aligned(workspace, 16)) return fail(TQ_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  return launch_tree_attention(kctx, vctx, group_off, ngroups, perm, table, page, q, q_dtype, kcache, vcache, seq_lens,
+                               draft_lens, tree_mask, B, T, Hq, Hkv, D, max_len, scale, out, workspace,
+                               (cudaStream_t)stream);
+}
+
+int tq_tree_mask(const int32_t* parent, int B, int T, uint64_t* mask) {
+  if (!parent || !mask || B < 0 || T < 1 || T > 256) return fail(TQ_ERR_INVALID_ARG, "tq_tree_mask: bad arguments");
+  const int W = (T + 63) / 64;
+  for (int b = 0; b < B; ++b)
+    for (int j = 0; j < T; ++j) {
+      const int p = parent[(size_t)b * T + j];
+      if (p < -1 || p >= j) return fail(TQ_ERR_INVALID_ARG, "tq_tree_mask: a parent must be in [-1, j)");
+    }
+  for (int b = 0; b < B; ++b)
+    for (int j = 0; j < T; ++j) {
+      const int p = parent[(size_t)b * T + j];
+      uint64_t* row = mask + ((size_t)b * T + j) * W;
+      for (int w = 0; w < W; ++w) row[w] = p >= 0 ? mask[((size_t)b * T + p) * W + w] : 0;
+      row[j >> 6] |= 1ull << (j & 63);
+    }
+  return TQ_OK;
 }
 
 }  // extern "C"
