@@ -144,6 +144,7 @@ void tq_free(tq_ctx* ctx);
  *            the stall injected by tq_debug_inject_stall)
  *   401-404  workspace quantize path: a pipeline wait exceeded its limit (idem)
  *   501-506  search: a pipeline wait exceeded its limit (idem)
+ *   601-612  tree attention: a pipeline wait exceeded its limit (idem)
  *   901      a device slot array (dst_slot / src_slot) held a slot outside [0, cap): that
  *            row was skipped (quantize) or written as zeros (dequantize)
  *   902      a channel permutation or column map held an entry out of range: that element
@@ -439,7 +440,7 @@ int tq_sparse_decode_attention(const tq_ctx* const* kctx, const tq_ctx* const* v
  * itself, for a tree; any mask is allowed).  A row that attends nothing, and every row j >= n_b, gives
  * zeros.  Accepted tokens are kept by quantizing them to their final slots; nothing else in the cache
  * changes.
- * q, out: device [B][T][Hq][D] of q_dtype (F32, BF16, F16); 1 <= T <= 256.  draft_lens: device int32 [B],
+ * q, out: device [B][T][Hq][D] of q_dtype (F32, BF16, F16), 16-byte aligned (and channel_perm); 1 <= T <= 256.  draft_lens: device int32 [B],
  * clamped to [0, min(T, seq_lens[b])], or NULL: T each.  tree_mask: device uint64 [B][T][(T+63)/64], or
  * NULL: a chain (row j attends the drafted tokens up to j).  The products run on fp16 operands with
  * 32-bit sums, so an F32 result is good to about 1e-3 as well.  Supported caches, other arguments,

@@ -722,8 +722,8 @@ int tq_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, cons
   if (r != TQ_OK) return r;
   if (B == 0) return TQ_OK;
   if ((r = check_cache_shape((int64_t)B * Hkv * ((Hq / Hkv + 3) / 4), (int64_t)B * T * Hq, max_len, "tq_tree_attention")) != TQ_OK) return r;
-  if (!aligned(out, elem_size(q_dtype)) || !aligned(q, elem_size(q_dtype)))
-    return fail(TQ_ERR_UNSUPPORTED, "q or out not aligned to its element");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(perm, 16) || !aligned(tree_mask, 8))
+    return fail(TQ_ERR_UNSUPPORTED, "q, out and the channel permutation must be 16-byte aligned, the mask 8-byte aligned");
   if (!decode_caches_supported(kctx, vctx, ngroups, kcache, vcache)) return unsupported_caches("tq_tree_attention");
   const size_t need = tree_workspace_bytes(B, T, Hq, Hkv, max_len);
   if (!workspace || ws_bytes < need) return fail(TQ_ERR_WORKSPACE, "workspace too small");

@@ -73,7 +73,11 @@ class Cache:
         Tolerance: keys, queries, levels and their products with norms are carried in 16-bit floats, whose relative
         rounding error is at most 2^-11 and 2e-4 in the mean square; four such factors make 4e-4.  A logit is a sum of
         128 products, so its error is 4e-4 scale |q| |k| / sqrt(128) in the mean square, independent from token to
-        token; a weight's relative error is that of its logit.  Weights and values carry the same 4e-4, and so does
+        token; a weight p_t's relative error e_t is that of its logit.  Channel c of the output then moves by
+        sum_t p_t e_t (v_tc - o_c), a sum of independent terms with these known factors: its deviation is the root of
+        the sum of their squares, channel by channel (an average over the channels would not do: one token's v_tc - o_c
+        is several times its own mean square in some channel).  The weights' own rounding moves it by p_t v_tc 2e-4.
+        The values' rounding happens in the rotated coordinates, so it spreads evenly over the channels, as does that of
         the last rotation.  Six standard deviations of each part are allowed."""
         ch = np.arange(D) if perm is None else np.asarray(perm[h])
         s = self.slots(b, h, tokens)
@@ -98,14 +102,16 @@ class Cache:
         e = np.where(keep, np.exp(logit - top[:, None]), 0.0)
         p = e / np.where(some, e.sum(1), 1.0)[:, None]
         o = p @ v
-        v2 = (v ** 2).sum(1)
-        far = np.maximum(v2[None] - 2 * o @ v.T + (o ** 2).sum(1)[:, None], 0)
-        dev = np.sqrt(((p * size * scale) ** 2 * far).sum(1) / D) + np.sqrt((p ** 2 * v2).sum(1) / D) + \
-            np.sqrt((o ** 2).sum(1) / D)
-        out = np.concatenate([o[:, self.off[g]:self.off[g + 1]] @ rot[g] for g in range(len(rot))], 1)
+        turn = lambda x: np.concatenate([x[:, self.off[g]:self.off[g + 1]] @ rot[g] for g in range(len(rot))], 1)  # noqa: E731
+        out, vt = turn(o), turn(v)
+        w2 = (p * size * scale) ** 2
+        moved = np.maximum(w2 @ vt ** 2 - 2 * out * (w2 @ vt) + out ** 2 * w2.sum(1)[:, None], 0)
+        even = np.sqrt((p ** 2 * (v ** 2).sum(1)).sum(1) / D) + np.sqrt((o ** 2).sum(1) / D)
+        dev = np.sqrt(moved) + np.sqrt(p ** 2 @ vt ** 2) + even[:, None]
         res = np.zeros_like(out)
-        res[:, ch] = out
-        return res, np.repeat(6 * 4e-4 * dev[:, None] + 1e-6, D, 1)
+        tol = np.zeros_like(out)
+        res[:, ch], tol[:, ch] = out, 6 * 4e-4 * dev + 1e-6
+        return res, tol
 
 
 # ------------------------------------------------------------------ the same caches on the GPU

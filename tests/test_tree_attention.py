@@ -258,8 +258,12 @@ def test_tree_plan_streams_graphs_and_refusals():
     sl.copy_(i32(64, 200))
     dl.copy_(i32(1, 5))
     graph.replay()
+    got = out.clone()                                       # (sequence 1 now reads unused slots: NaN on both sides)
+    assert torch.allclose(got, plan(q, sl, dl, mask, 0.1), rtol=0, atol=0, equal_nan=True) and not got[0].isnan().any()
+    sl.copy_(i32(130, 88))
+    graph.replay()
     got = out.clone()
-    assert torch.equal(got, plan(q, sl, dl, mask, 0.1))
+    assert torch.equal(got, plan(q, sl, dl, mask, 0.1)) and not got.isnan().any()
     for bad in (lambda: plan(q[:, :4], sl, dl, mask, 0.1), lambda: plan(q, sl.long(), dl, mask, 0.1),
                 lambda: plan(q, sl, dl[:1], mask, 0.1), lambda: plan(q, sl, dl, mask.int(), 0.1),
                 lambda: plan(q, sl, dl, mask[:, :, 0], 0.1), lambda: plan(q, sl, dl, mask, 0.1, out=out.float()),
