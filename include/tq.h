@@ -144,7 +144,7 @@ void tq_free(tq_ctx* ctx);
  *            the stall injected by tq_debug_inject_stall)
  *   401-404  workspace quantize path: a pipeline wait exceeded its limit (idem)
  *   501-506  search: a pipeline wait exceeded its limit (idem)
- *   601-612  tree attention: a pipeline wait exceeded its limit (idem)
+ *   601-614  tree attention: a pipeline wait exceeded its limit (idem)
  *   901      a device slot array (dst_slot / src_slot) held a slot outside [0, cap): that
  *            row was skipped (quantize) or written as zeros (dequantize)
  *   902      a channel permutation or column map held an entry out of range: that element

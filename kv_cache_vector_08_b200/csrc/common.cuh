@@ -76,6 +76,7 @@ struct tq_ctx {
   tq::Codebook cb{};
   int m = 0, mode = 0, bits = 0;
   float sqrt_pi_over_2_over_m = 0.f;  // QJL unbiasing constant sqrt(pi/2)/m
+  float lev_scale = 1.f;              // in [1, 2): the levels times this are nearly exact in fp16
   float s_rowmax = 0.f;               // max_j ||S_j||: bounds |(S q)_j| by s_rowmax * ||q||
   // device float32 copies (row-major): Pi for the decode merge's inverse rotation, the
   // transposes for the query projections (coalesced column access)

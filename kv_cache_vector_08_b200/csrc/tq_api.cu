@@ -196,6 +196,28 @@ void release(tq_ctx* c) {
   delete c;
 }
 
+// Factor in [1, 2) for which the positive levels times the factor are closest to fp16 numbers (the
+// smallest maximum of their relative rounding errors over 2^16 steps; up to 8 levels, where the first
+// try alone would leave up to 2^-11).
+float level_scale(const std::vector<double>& c) {
+  float best = 1.f;
+  double best_err = 1e300;
+  const size_t half = c.size() / 2;
+  for (int i = 0; i < 1 << 16; ++i) {
+    const float f = 1.f + (float)i / (1 << 16);
+    double err = 0.0;
+    for (size_t j = half; j < c.size() && err < best_err; ++j) {
+      const double v = c[j] * f;
+      err = std::max(err, std::fabs((double)__half2float(__float2half_rn((float)v)) - v) / v);
+    }
+    if (err < best_err) {
+      best_err = err;
+      best = f;
+    }
+  }
+  return best;
+}
+
 int check_args_common(int d, int bits, int mode) {
   if (mode != TQ_MODE_PROD && mode != TQ_MODE_MSE) return fail(TQ_ERR_INVALID_ARG, "mode must be TQ_MODE_PROD or TQ_MODE_MSE");
   if (d < 3 || d > 4096) return fail(TQ_ERR_UNSUPPORTED, "d must be in [3, 4096]");
@@ -332,6 +354,7 @@ int tq_init(tq_ctx** out, int d, int bits, uint64_t seed, int mode) {
     cb.t[j] = j < cb.K - 1 ? (float)h.boundaries[j] : INFINITY;
   }
   for (int code = 0; code < kMaxLevels; ++code) cb.cc[code] = code < cb.K ? cb.c[code_index(code, h.k)] : 0.f;
+  c->lev_scale = level_scale(h.centroids);
   c->sqrt_pi_over_2_over_m = mode == TQ_MODE_PROD ? (float)(std::sqrt(M_PI / 2.0) / h.m) : 0.f;
   for (int j = 0; j < h.m; ++j) {
     double r = 0.0;

@@ -12,14 +12,26 @@
 // all operands fp16, sums fp32; the norms of the channel groups ride on the operands, so one
 // product serves any grouping.
 //
-// CTA = 128 query rows of one (sequence, kv head) over one split of the tokens, two per SM; nine
-// warps.  First the rows are projected (two products of the rows with Pi and S).  Then, tile by
-// tile: warps 4-7 decode (thread = token x half of the head: code words come from global memory
-// a tile ahead, byte-permute lookups make fp16 levels, K is written K-major, V with the channels
-// contiguous as it lies in the cache); warp 8 issues the products; warps 0-3 (thread = row) turn
-// S into P in place in tensor memory with a running maximum that moves only when it grew by 2^8,
-// so that O, which stays in tensor memory, is seldom rescaled.  At the end O / l is rotated back
-// by one more product, and written (one split) or left as a partial for the merge kernel.
+// CTA = up to 128 query rows of one (sequence, kv head) over one split of the tokens, one per SM.
+// First the rows are projected (two products of the rows with Pi and S); Q then stays in tensor
+// memory as the A operand, because a product that fetches both operands from shared memory is
+// bound by that at 64 columns (measured: 768 cycles of a tile's S instead of 256).  Then a pipeline
+// of tiles, four deep in K, V and S:
+//   decoders (8 warps, two sets that take alternate tiles; thread = token x half of the head): code
+//     words come from global memory a tile ahead, byte-permute lookups make fp16 levels; K is
+//     written K-major, V with the channels contiguous, as it lies in the cache;
+//   products (one warp): S of tile i, then O += P V of tile i - 2;
+//   softmax (4 warps, thread = row): S to P in place in tensor memory, with a running maximum
+//     that moves only when it grew by 2^8, so that O, which stays in tensor memory, is seldom
+//     rescaled.
+// Rows that fill a half or a quarter of the 128 lanes are repeated in the others (fold 2 or 4), and
+// each copy takes every second or fourth tile: the lanes of the other copies put zeros into its P.
+// The products cost the same, the exponentials spread over all lanes.  The copies' sums meet at the
+// end.  At last O / l is rotated back by one more product, and written (one split) or left as a
+// partial for the merge kernel.
+//
+// The levels of a codebook enter scaled by a factor for which fp16 holds them almost exactly
+// (tq_init looks for it); the projection and the last product take the factor out.
 //
 // P carries a factor 2^7: between the 2^15 it can reach and the smallest fp16, weights down to
 // 2^-31 of the row's largest count.
@@ -44,20 +56,26 @@ using mmaops::prmt;
 constexpr int kTD = 128;          // head dimension
 constexpr int kTileTok = 64;      // tokens per tile: a tile never crosses a page
 constexpr int kRows = 128;        // query rows per CTA
-constexpr int kSoftWarps = 4, kDecWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kDecWarps + 1);
-constexpr int kSoft = 32 * kSoftWarps, kDec = 32 * kDecWarps;
+constexpr int kSoftWarps = 4, kDecWarps = 8, kMmaWarp = kSoftWarps + kDecWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kDecSet = kDecWarps / 2;      // warps that decode one tile
+constexpr int kStages = 4;                  // tiles in flight (K, V, S)
+constexpr int kAhead = 2;                   // S runs this many tiles ahead of O += P V
 constexpr uint64_t kDrainNs = 2000000000ull;
 
-// shared memory: the Q operand (first: rows and Pi for the projection), K and V operands
-constexpr int kQBytes = kRows * 512, kKBytes = kTileTok * 512, kVBytes = kTileTok * 256;
-constexpr int kOffK = kQBytes, kOffV = kOffK + kKBytes, kOffMisc = kOffV + kVBytes;
-constexpr int kSmem = kOffMisc + 1024;
-// tensor memory columns: S / P of even and odd tiles, O; the projections use all of them
-constexpr int kTmemCols = 256, kColO = 128;
+// shared memory: K and V stages (first: the rows, 16 Pi and 16 kappa S of the projection; at the end:
+// Pi of the values and the copies' results)
+constexpr int kKBytes = kTileTok * 512, kVBytes = kTileTok * 256;
+constexpr int kOffV = kStages * kKBytes, kOffMisc = kOffV + kStages * kVBytes;
+constexpr int kSmem = kOffMisc + 2048;
+constexpr int kOffPi = 32768, kOffS = 65536;             // of the projection
+constexpr int kOffSum = 32768;                           // copies' results, rows of kSumLd floats
+constexpr int kSumLd = 132;
+// tensor memory columns: Q, O, four S / P buffers (the projections use the latter)
+constexpr int kTmemCols = 512, kColQ = 0, kColO = 128, kColS = 256;
 
-constexpr float kPShift = 7.f;    // P = 2^(l - m + 7)
-constexpr float kGrow = 8.f;      // growth of the maximum (log2) that rescales O
+constexpr float kPShift = 3.f;    // P = 2^(l - m + 3)
+constexpr float kGrow = 12.f;     // growth of the maximum (log2) that rescales O
 
 struct TreeGroup {
   const uint8_t* kcodes;
@@ -66,17 +84,17 @@ struct TreeGroup {
   const uint16_t* vnorm;
   uint32_t klo[2], khi[2];        // fp16 bytes of the signed level of each key code
   uint32_t vlo[2], vhi[2];        // fp16 bytes of the magnitudes of the value levels
+  float kinv, vinv;               // 1 / (16 factor) of the key and value levels
   const __half *pi, *st, *piv;    // 16 Pi^T, 16 sqrt(pi/2)/d S^T of the keys, 16 Pi^T of the values ([d][d] fp16)
 };
 
 struct TreeArgs {
   TreeGroup g[2];
-  int B, T, Hq, Hkv, rep, R, tiles_r, nsplit, chunk, words;
+  int B, T, Hq, Hkv, rep, R, fold, tiles_r, nsplit, chunk, words;
   int64_t max_len, npages;
   float scale_log2;               // |scale| log2(e)
   float sign;                     // sign of the scale
   const void* q;
-  int q_dtype;
   void* out;
   const int32_t *seq_lens, *draft_lens;
   const uint64_t* mask;
@@ -84,45 +102,55 @@ struct TreeArgs {
   int page, max_pages;
   float* part;                    // [B Hkv R][nsplit][128] rotated partial results
   float2* ml;                     // [B Hkv R][nsplit] (maximum in log2, sum)
-  uint64_t wait_ns;
+  uint64_t wait;                  // limit of a wait, in SM cycles
   int* err;
 };
 
-__device__ __forceinline__ float load_any(const void* p, int dtype, size_t i) {
-  if (dtype == TQ_DTYPE_F32) return static_cast<const float*>(p)[i];
-  if (dtype == TQ_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-__device__ __forceinline__ void store_any(void* p, int dtype, size_t i, float v) {
-  if (dtype == TQ_DTYPE_F32) static_cast<float*>(p)[i] = v;
-  else if (dtype == TQ_DTYPE_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
-// four consecutive elements (16- or 8-byte aligned)
-__device__ __forceinline__ float4 load_any4(const void* p, int dtype, size_t i) {
-  if (dtype == TQ_DTYPE_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-  if (dtype == TQ_DTYPE_BF16)
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xFFFF0000u));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ void store_any4(void* p, int dtype, size_t i, float4 v) {
-  if (dtype == TQ_DTYPE_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <typename T>
+struct alignas(4 * sizeof(T)) Four {
+  T v[4];
+};
+// Four consecutive channels 4 lane .. of an output row, or (perm: the kv head's permutation) the
+// channels that the row's group coordinates 4 lane .. stand for.
+template <typename T>
+__device__ __forceinline__ void store_row(T* row, const int32_t* perm, int lane, float4 v) {
+  Four<T> x;
+  x.v[0] = from_f<T>(v.x);
+  x.v[1] = from_f<T>(v.y);
+  x.v[2] = from_f<T>(v.z);
+  x.v[3] = from_f<T>(v.w);
+  if (!perm) {
+    *reinterpret_cast<Four<T>*>(row + 4 * lane) = x;
     return;
   }
-  uint2 w;
-  if (dtype == TQ_DTYPE_BF16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-    w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = w;
+  const int4 to = __ldg(reinterpret_cast<const int4*>(perm) + lane);
+  if (to.x >= 0 && to.x < kTD) row[to.x] = x.v[0];
+  if (to.y >= 0 && to.y < kTD) row[to.y] = x.v[1];
+  if (to.z >= 0 && to.z < kTD) row[to.z] = x.v[2];
+  if (to.w >= 0 && to.w < kTD) row[to.w] = x.v[3];
 }
+// 16 bytes from global to shared memory, asynchronously
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t h2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -131,6 +159,27 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// (a.x s + t, a.y s + t) and pairwise sums, two lanes of 32 bits an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 s, float2 t) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&s)),
+        "l"(*reinterpret_cast<const uint64_t*>(&t)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
 }
 __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -161,64 +210,93 @@ constexpr uint32_t kMajorN = 1u << 16;     // instruction descriptor: B has N co
 // 16-byte chunk c of a 128-byte row, swizzled
 __device__ __forceinline__ uint32_t swz(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
 
-// A [rows][64 blocks] fp16 matrix of `cols` columns (a multiple of 64) into swizzled blocks of
-// 64 columns, `rows` 128-byte rows each.
-__device__ __forceinline__ void copy_matrix(uint8_t* dst, const __half* src, int rows, int cols, int t, int nt) {
-  const int per = cols / 8;
-  for (int e = t; e < rows * per; e += nt) {
-    const int r = e / per, c = e - r * per;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + e);
-    *reinterpret_cast<uint4*>(dst + (c >> 3) * rows * 128 + swz(r, c & 7)) = v;
+// Every n-th 16-byte piece of a square fp16 matrix of width 64 or 128, into swizzled blocks of 64
+// columns with 128-byte rows.  (Rolled: code that runs once a CTA must not push the loops out of the
+// instruction cache.  With everything unrolled the kernel had 144 KB of code, and ran 5 times slower.)
+template <int W>
+__device__ __forceinline__ void copy_matrix(uint8_t* dst, const __half* src, int t, int nt) {
+#pragma unroll 1
+  for (int e = t; e < W * W / 8; e += nt) {
+    const int r = e / (W / 8), c = e % (W / 8);
+    copy16(dst + (c >> 3) * W * 128 + swz(r, c & 7), src + (size_t)e * 8);
   }
 }
 
+// Bounded wait for an mbarrier phase, compact: it is inlined many times.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, int parity, const volatile int* abort, uint64_t limit) {
+  const uint32_t p = (uint32_t)parity & 1u;
+  if (mbar_try_wait(bar, p)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, p))
+    if (*abort || (uint64_t)(clock64() - t0) > limit) return false;
+  return true;
+}
+
 // The code words of one thread's 64 coordinates (two 32-coordinate groups of P words).
+// (volatile: the compiler would move a plain load down to its use, behind the waits that it is to overlap)
+__device__ __forceinline__ uint4 ld_ahead16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_ahead8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_ahead2(const void* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];\n" : "=h"(v) : "l"(p));
+  return v;
+}
 template <int P>
-struct Words {
-  uint32_t w[2 * P];
-};
-template <int P>
-__device__ __forceinline__ void load_words(Words<P>& x, const uint8_t* rec) {
+__device__ __forceinline__ void load_words(uint32_t (&x)[8], const uint8_t* rec) {
   if constexpr (P == 3) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(rec) + i);
-      x.w[2 * i] = v.x;
-      x.w[2 * i + 1] = v.y;
+      const uint2 v = ld_ahead8(rec + 8 * i);
+      x[2 * i] = v.x;
+      x[2 * i + 1] = v.y;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(rec) + i);
-      x.w[4 * i] = v.x; x.w[4 * i + 1] = v.y; x.w[4 * i + 2] = v.z; x.w[4 * i + 3] = v.w;
+      const uint4 v = ld_ahead16(rec + 16 * i);
+      x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
     }
   }
 }
-// Byte-permute selectors (low code bits) of slice u of group g, and its top bits at byte msbs.
+// Byte-permute selectors (low code bits) of slice u of the first group, and its top bits at byte msbs.
 template <int P>
-__device__ __forceinline__ uint32_t low_sel(const Words<P>& x, int g, int u) {
-  if constexpr (P == 4) return x.w[4 * g + u] & 0x77777777u;
-  else if constexpr (P == 3) return (x.w[3 * g + (u & 1)] >> (2 * (u >> 1))) & 0x33333333u;
-  else return (x.w[2 * g] >> u) & 0x11111111u;
+__device__ __forceinline__ uint32_t low_sel(const uint32_t (&x)[P], int u) {
+  if constexpr (P == 4) return x[u] & 0x77777777u;
+  else if constexpr (P == 3) return (x[u & 1] >> (2 * (u >> 1))) & 0x33333333u;
+  else return (x[0] >> u) & 0x11111111u;
 }
 template <int P>
-__device__ __forceinline__ uint32_t top_bits(const Words<P>& x, int g, int u, int h) {
-  if constexpr (P == 4) return h ? x.w[4 * g + u] << 4 : x.w[4 * g + u];
-  else return x.w[P * g + P - 1] << (2 * u + h);
+__device__ __forceinline__ uint32_t top_bits(const uint32_t (&x)[P], int u, int h) {
+  if constexpr (P == 4) return h ? x[u] << 4 : x[u];
+  else return x[P - 1] << (2 * u + h);
 }
 
-// Key rows: levels times the norm, and the residual signs times both norms.
+// Key rows: levels times the norm, and the residual signs times both norms.  (The loop over the
+// two groups is not unrolled: the warps of a CTA run different code, and short loops keep it in
+// the instruction cache.)
 template <int P>
-__device__ __forceinline__ void decode_keys(const Words<P>& x, const TreeGroup& t, float n, float rn, uint8_t* lev,
+__device__ __forceinline__ void decode_keys(const uint32_t (&x)[8], const TreeGroup& t, float n, float rn, uint8_t* lev,
                                             uint8_t* sgn, int row) {
   const uint32_t nn = h2_bits(n, n);
   const uint32_t rr = h2_bits(n * rn, n * rn) | 0x80008000u;    // (a set sign bit turns it positive)
   const int sw = row & 7;
+  uint32_t y[P];
 #pragma unroll
-  for (int g = 0; g < 2; ++g)
+  for (int i = 0; i < P; ++i) y[i] = x[i];
+#pragma unroll 1
+  for (int g = 0; g < 2; ++g) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const uint32_t sel = low_sel<P>(x, g, u);
+      const uint32_t sel = low_sel<P>(y, u);
       uint32_t o[4], s[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -226,7 +304,7 @@ __device__ __forceinline__ void decode_keys(const Words<P>& x, const TreeGroup& 
         const uint32_t lb = prmt(t.klo[0], t.klo[1], sl), hb = prmt(t.khi[0], t.khi[1], sl);
         o[2 * h] = mul_h2(prmt(lb, hb, 0x5140u), nn);
         o[2 * h + 1] = mul_h2(prmt(lb, hb, 0x7362u), nn);
-        const uint32_t tb = top_bits<P>(x, g, u, h);
+        const uint32_t tb = top_bits<P>(y, u, h);
         s[2 * h] = (prmt(tb, 0u, 0x1404u) & 0x80008000u) ^ rr;
         s[2 * h + 1] = (prmt(tb, 0u, 0x3424u) & 0x80008000u) ^ rr;
       }
@@ -234,112 +312,153 @@ __device__ __forceinline__ void decode_keys(const Words<P>& x, const TreeGroup& 
       *reinterpret_cast<uint4*>(lev + c) = make_uint4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<uint4*>(sgn + c) = make_uint4(s[0], s[1], s[2], s[3]);
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i) y[i] = x[P + i];
+  }
 }
 // Value rows: levels times the norm.
 template <int P>
-__device__ __forceinline__ void decode_values(const Words<P>& x, const TreeGroup& t, float n, uint8_t* dst, int row) {
+__device__ __forceinline__ void decode_values(const uint32_t (&x)[8], const TreeGroup& t, float n, uint8_t* dst, int row) {
   const uint32_t nn = h2_bits(n, n);
   const int sw = row & 7;
+  uint32_t y[P];
 #pragma unroll
-  for (int g = 0; g < 2; ++g)
+  for (int i = 0; i < P; ++i) y[i] = x[i];
+#pragma unroll 1
+  for (int g = 0; g < 2; ++g) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const uint32_t sel = low_sel<P>(x, g, u);
+      const uint32_t sel = low_sel<P>(y, u);
       uint32_t o[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t sl = h ? sel >> 16 : sel;
         const uint32_t lb = prmt(t.vlo[0], t.vlo[1], sl);
-        const uint32_t hb = prmt(t.vhi[0], t.vhi[1], sl) ^ (top_bits<P>(x, g, u, h) & 0x80808080u);
+        const uint32_t hb = prmt(t.vhi[0], t.vhi[1], sl) ^ (top_bits<P>(y, u, h) & 0x80808080u);
         o[2 * h] = mul_h2(prmt(lb, hb, 0x5140u), nn);
         o[2 * h + 1] = mul_h2(prmt(lb, hb, 0x7362u), nn);
       }
       *reinterpret_cast<uint4*>(dst + (((4 * g + u) ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i) y[i] = x[P + i];
+  }
 }
 
 struct Bars {
-  uint64_t proj, kfull, kempty, vfull, vempty, sfull[2], pfull[2], wfull, ofull, dfull, drain;
+  uint64_t proj, klast, wfull, xfull, ofull, dfull, drain;
+  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[kStages], pfull[kStages];
 };
 
-// The decoder warps of one half of the head: K of tile i + 1 before V of tile i, so that the
-// next tile's logits are under way while this tile's weights are formed.
+// One decoder thread: token `row` and one half of the head, of tiles set, set + 2, ...  Its code
+// words and norms of the next tile come from memory while it decodes this one.
+struct Decoder {
+  uint32_t kw[8], vw[8];
+  uint16_t kn, kr, vn;
+  int64_t slot;                 // of the next tile's token, -1 past the end
+  int tok, pi, po, pg;          // the token after that: page entry, offset, page
+};
+
 template <int PK, int PV, bool TWO>
-__device__ __forceinline__ bool decode_loop(const TreeArgs& A, const TreeGroup& g, uint8_t* smem, Bars* bar, int half,
-                                            int row, int b, int hk, int t0, int t1, int n, const volatile int* abort_v,
-                                            int& code) {
-  uint8_t* lev = smem + kOffK + half * (kTileTok * 128) + row * 128;
-  uint8_t* sgn = lev + 2 * (kTileTok * 128);
-  uint8_t* val = smem + kOffV + half * (kTileTok * 128) + row * 128;
-  const int64_t slot0 = ((int64_t)b * A.Hkv + hk) * A.max_len;
-  auto slot_of = [&](int i) -> int64_t {       // slot of this thread's token of tile i, or -1
-    const int t = t0 + i * kTileTok + row;
-    if (i >= n || t >= t1) return -1;
-    if (!A.table) return slot0 + t;
-    int pg = __ldg(A.table + (size_t)b * A.max_pages + t / A.page);
-    if (pg < 0 || pg >= A.npages) {
-      if (A.err) atomicCAS(A.err, 0, (int)kErrSlotRange);
-      pg = 0;
-    }
-    return ((int64_t)pg * A.Hkv + hk) * A.page + t % A.page;
-  };
-  Words<PK> kw;
-  Words<PV> vw;
-  uint16_t kn = 0, kr = 0, vn = 0;
-  // bytes of a record, and of this half's part of it
-  constexpr int kRec = TWO ? PK * 8 : PK * 16, vRec = TWO ? PV * 8 : PV * 16;
-  const int kOff = TWO ? 0 : half * PK * 8, vOff = TWO ? 0 : half * PV * 8;
-  auto load_k = [&](int64_t s) {
-    kn = kr = 0;
+struct Decode {
+  // bytes of a record, and of a half's part of it
+  static constexpr int kRec = TWO ? PK * 8 : PK * 16, vRec = TWO ? PV * 8 : PV * 16;
+  static constexpr int kPart = TWO ? 0 : PK * 8, vPart = TWO ? 0 : PV * 8;
+
+  __device__ static __forceinline__ void load_k(Decoder& x, const TreeGroup& g, int half) {
+    x.kn = x.kr = 0;
 #pragma unroll
-    for (int i = 0; i < 2 * PK; ++i) kw.w[i] = 0u;
-    if (s >= 0) {
-      load_words<PK>(kw, g.kcodes + s * kRec + kOff);
-      kn = __ldg(g.knorm + s);
-      kr = __ldg(g.krnorm + s);
-    }
-  };
-  auto load_v = [&](int64_t s) {
-    vn = 0;
-#pragma unroll
-    for (int i = 0; i < 2 * PV; ++i) vw.w[i] = 0u;
-    if (s >= 0) {
-      load_words<PV>(vw, g.vcodes + s * vRec + vOff);
-      vn = __ldg(g.vnorm + s);
-    }
-  };
-  auto f = [](uint16_t x) { return __half2float(__ushort_as_half(x)); };
-  int64_t s1 = slot_of(0);
-  load_k(s1);
-  load_v(s1);
-  for (int i = 0; i <= n; ++i) {
-    const int64_t sv = s1;
-    if (i < n) {
-      s1 = slot_of(i + 1);
-      if (!mbar_wait(&bar->kempty, (uint32_t)((i & 1) ^ 1), abort_v, A.wait_ns)) { code = 601; return false; }
-      decode_keys<PK>(kw, g, f(kn), f(kr), lev, sgn, row);
-      fence_proxy_async_smem();
-      mbar_arrive(&bar->kfull);
-      load_k(s1);
-    }
-    if (i > 0) {
-      if (!mbar_wait(&bar->vempty, (uint32_t)(((i - 1) & 1) ^ 1), abort_v, A.wait_ns)) { code = 602; return false; }
-      decode_values<PV>(vw, g, f(vn), val, row);
-      fence_proxy_async_smem();
-      mbar_arrive(&bar->vfull);
-      if (i < n) load_v(sv);
+    for (int i = 0; i < 2 * PK; ++i) x.kw[i] = 0u;
+    if (x.slot >= 0) {
+      load_words<PK>(x.kw, g.kcodes + x.slot * kRec + half * kPart);
+      x.kn = ld_ahead2(g.knorm + x.slot);
+      x.kr = ld_ahead2(g.krnorm + x.slot);
     }
   }
-  return true;
-}
+  __device__ static __forceinline__ void load_v(Decoder& x, const TreeGroup& g, int half) {
+    x.vn = 0;
+#pragma unroll
+    for (int i = 0; i < 2 * PV; ++i) x.vw[i] = 0u;
+    if (x.slot >= 0) {
+      load_words<PV>(x.vw, g.vcodes + x.slot * vRec + half * vPart);
+      x.vn = ld_ahead2(g.vnorm + x.slot);
+    }
+  }
+  // Slot of the token, two tiles further with every call; the page entry of a call is loaded by
+  // the call before.
+  __device__ static __forceinline__ void advance(Decoder& x, const TreeArgs& A, int b, int hk, int t1) {
+    if (x.tok >= t1) {
+      x.slot = -1;
+      return;
+    }
+    if (!A.table) {
+      x.slot = ((int64_t)b * A.Hkv + hk) * A.max_len + x.tok;
+      x.tok += 2 * kTileTok;
+      return;
+    }
+    if (x.pg < 0 || x.pg >= A.npages) {
+      if (A.err) atomicCAS(A.err, 0, (int)kErrSlotRange);
+      x.pg = 0;
+    }
+    x.slot = ((int64_t)x.pg * A.Hkv + hk) * A.page + x.po;
+    x.tok += 2 * kTileTok;
+    if (x.tok < t1) {
+      const int was = x.pi;
+      x.po += 2 * kTileTok;
+#pragma unroll 1
+      while (x.po >= A.page) { x.po -= A.page; ++x.pi; }
+      if (x.pi != was) x.pg = __ldg(A.table + (size_t)b * A.max_pages + x.pi);
+    }
+  }
+  __device__ static __forceinline__ void start(Decoder& x, const TreeArgs& A, const TreeGroup& g, int half, int tok, int b,
+                                               int hk, int t1) {
+    x.tok = tok;
+    x.pi = A.table ? tok / A.page : 0;
+    x.po = A.table ? tok - x.pi * A.page : 0;
+    x.pg = A.table && tok < t1 ? __ldg(A.table + (size_t)b * A.max_pages + x.pi) : 0;
+    advance(x, A, b, hk, t1);
+    load_k(x, g, half);
+    load_v(x, g, half);
+  }
+  __device__ static __forceinline__ bool loop(Decoder& x, const TreeArgs& A, const TreeGroup& g, uint8_t* smem, Bars* bar,
+                                              int half, int set, int row, int b, int hk, int t1, int n,
+                                              const volatile int* abort_v, int& code) {
+    const uint32_t part = half * (kTileTok * 128) + row * 128;
+    const bool lane0 = (threadIdx.x & 31) == 0;
+    auto wait = [&](uint64_t* p, int parity) {
+      return __all_sync(0xffffffffu, bar_wait(p, parity, abort_v, A.wait)) != 0;
+    };
+    auto f = [](uint16_t h) { return __half2float(__ushort_as_half(h)); };
+#pragma unroll 1
+    for (int i = set; i < n; i += 2) {
+      const int st = i % kStages, ph = i / kStages;
+      advance(x, A, b, hk, t1);
+      if (!wait(&bar->kempty[st], ph + 1)) { code = 601; return false; }
+      uint8_t* lev = smem + st * kKBytes + part;
+      decode_keys<PK>(x.kw, g, f(x.kn), f(x.kr), lev, lev + 2 * (kTileTok * 128), row);
+      load_k(x, g, half);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane0) mbar_arrive(&bar->kfull[st]);
+      if (!wait(&bar->vempty[st], ph + 1)) { code = 602; return false; }
+      decode_values<PV>(x.vw, g, f(x.vn), smem + kOffV + st * kVBytes + part, row);
+      load_v(x, g, half);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane0) mbar_arrive(&bar->vfull[st]);
+    }
+    return true;
+  }
+};
 
-template <int PK0, int PV0, int PK1, int PV1, bool TWO>
-__global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const TreeArgs A) {
+template <int PK0, int PV0, int PK1, int PV1, bool TWO, typename T>
+__global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_constant__ TreeArgs A) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bar = reinterpret_cast<Bars*>(smem + kOffMisc);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + sizeof(Bars));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 512 - 8);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  float* s_scale = reinterpret_cast<float*>(smem + kOffMisc + 512);      // [128] logit scale of a row
+  float* s_scale = reinterpret_cast<float*>(smem + kOffMisc + 512);      // [128] logit scale of a lane's row
+  float2* s_ml = reinterpret_cast<float2*>(smem + kOffMisc + 1024);      // [128] the copies' maxima and sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % A.nsplit;
   const int rt = (blockIdx.x / A.nsplit) % A.tiles_r;
@@ -351,135 +470,150 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const TreeArgs A
   const int nrow = min(kRows, A.R - r0);                 // rows of this tile
   const int live = min(nrow, nd * A.rep - r0);           // those of drafted tokens that exist
   const int t0 = split * A.chunk, t1 = min(len, t0 + A.chunk);
+  const int32_t* perm = A.perm ? A.perm + (size_t)hk * kTD : nullptr;
   if (live <= 0 || t0 >= t1) {                           // nothing to attend: zeros (the merge writes its own)
     if (A.nsplit == 1)
-      for (int e = threadIdx.x; e < nrow * kTD; e += kThreads)
-        store_any(A.out, A.q_dtype, q_row(A, b, hk, r0 + e / kTD) * kTD + e % kTD, 0.f);
+#pragma unroll 1
+      for (int r = warp; r < nrow; r += kThreads / 32)
+        store_row<T>(static_cast<T*>(A.out) + q_row(A, b, hk, r0 + r) * kTD, nullptr, lane, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
   const int n = (t1 - t0 + kTileTok - 1) / kTileTok;
+  const int fold = A.fold, per = kRows / fold;           // copies of the rows, lanes of a copy
   if (threadIdx.x == 0) {
     mbar_init(&bar->proj, 1);
-    mbar_init(&bar->kfull, kDec);
-    mbar_init(&bar->kempty, 1);
-    mbar_init(&bar->vfull, kDec);
-    mbar_init(&bar->vempty, 1);
-    for (int i = 0; i < 2; ++i) {
+    mbar_init(&bar->klast, 1);
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar->kfull[i], kDecSet);
+      mbar_init(&bar->kempty[i], 1);
+      mbar_init(&bar->vfull[i], kDecSet);
+      mbar_init(&bar->vempty[i], 1);
       mbar_init(&bar->sfull[i], 1);
-      mbar_init(&bar->pfull[i], kSoft);
+      mbar_init(&bar->pfull[i], kSoftWarps);
     }
-    mbar_init(&bar->wfull, kDec);
-    mbar_init(&bar->ofull, kSoft);
+    mbar_init(&bar->wfull, kDecWarps);
+    mbar_init(&bar->xfull, kSoftWarps);
+    mbar_init(&bar->ofull, kSoftWarps);
     mbar_init(&bar->dfull, 1);
     mbar_init(&bar->drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kSoftWarps + kDecWarps) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  // ------------------------------------------------------------------ projection of the rows
-  // rows (fp16, scaled by a power of two so that the largest element is near 2^9) at 0, 16 Pi at
-  // 32 KB, 16 kappa S in the K buffer
-  copy_matrix(smem + 32768, A.g[0].pi, TWO ? 64 : 128, TWO ? 64 : 128, threadIdx.x, kThreads);
-  copy_matrix(smem + kOffK, A.g[0].st, TWO ? 64 : 128, TWO ? 64 : 128, threadIdx.x, kThreads);
-  if (TWO) {
-    copy_matrix(smem + 32768 + 8192, A.g[1].pi, 64, 64, threadIdx.x, kThreads);
-    copy_matrix(smem + kOffK + 8192, A.g[1].st, 64, 64, threadIdx.x, kThreads);
-  }
-  for (int r = warp; r < kRows; r += kThreads / 32) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < live) {
-      const size_t base = q_row(A, b, hk, r0 + r) * kTD;
-      if (A.perm) {
-        const int4 ch = __ldg(reinterpret_cast<const int4*>(A.perm + (size_t)hk * kTD) + lane);
-        auto get = [&](int c) {
-          if (c >= 0 && c < kTD) return load_any(A.q, A.q_dtype, base + c);
-          if (A.err) atomicCAS(A.err, 0, (int)kErrPermRange);
-          return 0.f;
-        };
-        v = make_float4(get(ch.x), get(ch.y), get(ch.z), get(ch.w));
-      } else {
-        v = load_any4(A.q, A.q_dtype, base + 4 * lane);
-      }
-    }
-    float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const int e = mx > 0.f && mx < INFINITY ? max(-110, min(110, 9 - ilogbf(mx))) : 0;
-    const float up = ldexpf(A.sign, e);
-    *reinterpret_cast<uint2*>(smem + (lane >> 4) * (kRows * 128) + swz(r, (lane >> 1) & 7) + 8 * (lane & 1)) =
-        make_uint2(h2_bits(v.x * up, v.y * up), h2_bits(v.z * up, v.w * up));
-    if (lane == 0) s_scale[r] = ldexpf(A.scale_log2, -e);
-  }
-  fence_proxy_async_smem();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   const volatile int* abort_v = abort_flag;
   auto fail = [&](int code) {
     atomicExch(abort_flag, 1);
     if (A.err) atomicCAS(A.err, 0, code);
   };
-  auto wait = [&](uint64_t* x, uint32_t parity) { return mbar_wait(x, parity, abort_v, A.wait_ns); };
   // the same answer for the whole warp, which the tensor memory accesses behind it need
-  auto wait_all = [&](uint64_t* x, uint32_t parity) { return __all_sync(0xffffffffu, wait(x, parity)) != 0; };
-  bool ok = true;
-  if (warp == kSoftWarps + kDecWarps && lane == 0) {
-    // D columns 64 j: coordinates 64 j .. of Pi q, then (from 128 on) of kappa S q
-    const uint32_t idesc = idesc_f16(kRows, 64, 0) | kMajorN;
-    const uint32_t a0 = smem_u32(smem);
-    for (int part = 0; part < 2; ++part)
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t w = part ? smem_u32(smem + kOffK) : a0 + 32768;
-        const uint32_t d = tmem + (uint32_t)(128 * part + 64 * j);
-        for (int ks = 0; ks < (TWO ? 4 : 8); ++ks) {
-          const uint32_t a = TWO ? a0 + j * (kRows * 128) + ks * 32 : a0 + (ks >> 2) * (kRows * 128) + (ks & 3) * 32;
-          const uint32_t bb = w + j * (TWO ? 8192 : 16384) + ks * 2048;
-          mma_ss(d, desc_sw128(a), desc_mn(bb, 8192), idesc, ks ? 1u : 0u);
-        }
-      }
-    mma_commit(&bar->proj);
+  auto wait_all = [&](uint64_t* x, int parity) { return __all_sync(0xffffffffu, bar_wait(x, parity, abort_v, A.wait)) != 0; };
+  uint32_t tmem = 0;
+  // ------------------------------------------------------------------ projection of the rows
+  // Rows and matrices come in as asynchronous copies; then a warp a row makes fp16 operands of them,
+  // scaled by a power of two so that the largest element is near 2^9, every copy of them.
+  const int dw = warp - kSoftWarps, half = (dw % kDecSet) >> 1, set = dw / kDecSet, drow = 32 * (dw & 1) + lane;
+  Decoder dec;
+  if (warp >= kSoftWarps && warp < kMmaWarp) {
+    const int tok = t0 + set * kTileTok + drow;
+    if (!TWO || half == 0) Decode<PK0, PV0, TWO>::start(dec, A, A.g[0], half, tok, b, hk, t1);
+    else Decode<PK1, PV1, TWO>::start(dec, A, A.g[1], 1, tok, b, hk, t1);
   }
-  __syncwarp();
-  if (!wait_all(&bar->proj, 0)) { fail(603); ok = false; }
-  tc_fence_after();
-  if (ok && warp < kSoftWarps + kDecWarps) {
-    // warps 0-3: Pi q, warps 4-7: kappa S q; row = lane of the warp's quarter
-    const int part = warp >> 2, r = 32 * (warp & 3) + lane;
-    const uint32_t src = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(128 * part);
+  bool ok = true;
+  {
+    copy_matrix<TWO ? 64 : 128>(smem + kOffPi, A.g[0].pi, threadIdx.x, kThreads);
+    copy_matrix<TWO ? 64 : 128>(smem + kOffS, A.g[0].st, threadIdx.x, kThreads);
+    if (TWO) {
+      copy_matrix<64>(smem + kOffPi + 8192, A.g[1].pi, threadIdx.x, kThreads);
+      copy_matrix<64>(smem + kOffS + 8192, A.g[1].st, threadIdx.x, kThreads);
+    }
+    constexpr int kChunks = kTD * (int)sizeof(T) / 16;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < live * kChunks; e += kThreads) {
+      const int r = e / kChunks, c = e % kChunks;
+      copy16(smem + kOffV + e * 16, static_cast<const uint8_t*>(A.q) + q_row(A, b, hk, r0 + r) * kTD * sizeof(T) + c * 16);
+    }
+    copy_wait();
+    __syncthreads();
+    int4 ch = make_int4(4 * lane, 4 * lane + 1, 4 * lane + 2, 4 * lane + 3);
+    if (perm) ch = __ldg(reinterpret_cast<const int4*>(perm) + lane);
+    const bool in = (unsigned)ch.x < kTD && (unsigned)ch.y < kTD && (unsigned)ch.z < kTD && (unsigned)ch.w < kTD;
+    if (!in && A.err) atomicCAS(A.err, 0, (int)kErrPermRange);
+#pragma unroll 1
+    for (int r = warp; r < per; r += kThreads / 32) {
+      const T* x = reinterpret_cast<const T*>(smem + kOffV) + r * kTD;
+      auto get = [&](int c) { return r < live && (unsigned)c < kTD ? to_f<T>(x[c]) : 0.f; };
+      const float4 v = make_float4(get(ch.x), get(ch.y), get(ch.z), get(ch.w));
+      float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t v[32];
-      tmem_ld32(src + 32 * c, v);
-      tmem_ld_wait();
-      uint8_t* dst = smem + (2 * part + (c >> 1)) * (kRows * 128);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = h2_bits(__uint_as_float(v[8 * k + 2 * i]) * (1.f / 16.f), __uint_as_float(v[8 * k + 2 * i + 1]) * (1.f / 16.f));
-        *reinterpret_cast<uint4*>(dst + swz(r, 4 * (c & 1) + k)) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // 2^e as a float, e in [-110, 110]
+      const int e = mx > 0.f && mx < INFINITY ? max(-110, min(110, 136 - (int)(__float_as_uint(mx) >> 23))) : 0;
+      const float up = A.sign * __uint_as_float((uint32_t)(127 + e) << 23);
+      const uint2 h = make_uint2(h2_bits(v.x * up, v.y * up), h2_bits(v.z * up, v.w * up));
+#pragma unroll 1
+      for (int c = r; c < kRows; c += per) {
+        *reinterpret_cast<uint2*>(smem + (lane >> 4) * (kRows * 128) + swz(c, (lane >> 1) & 7) + 8 * (lane & 1)) = h;
+        // (not 0: a column left out is -inf before the scale)
+        if (lane == 0) s_scale[c] = fmaxf(A.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1e-30f);
       }
     }
     fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem = *tmem_slot;
+    if (warp == kMmaWarp) {
+      // D columns 64 j: coordinates 64 j .. of Pi q, then (from 128 on) of kappa S q
+      constexpr uint32_t idesc = idesc_f16(kRows, 64, 0) | kMajorN;
+      const uint32_t a0 = smem_u32(smem);
+#pragma unroll 1
+      for (int pj = 0; pj < 4; ++pj) {
+        const int part = pj >> 1, j = pj & 1;
+#pragma unroll
+        for (int ks = 0; ks < (TWO ? 4 : 8); ++ks) {
+          const uint32_t a = TWO ? a0 + j * (kRows * 128) + ks * 32 : a0 + (ks >> 2) * (kRows * 128) + (ks & 3) * 32;
+          const uint32_t bb = a0 + (part ? kOffS : kOffPi) + j * (TWO ? 8192 : 16384) + ks * 2048;
+          mma_ss_warp(tmem + (uint32_t)(kColS + 64 * pj), desc_sw128(a), desc_mn(bb, 8192), idesc, ks ? 1u : 0u);
+        }
+      }
+      mma_commit_warp(&bar->proj);
+    }
+    if (!wait_all(&bar->proj, 0)) { fail(603); ok = false; }
+    tc_fence_after();
+    if (ok && warp < 8) {
+      // warps 0-3: Pi q to columns 0 .. 63 of Q, warps 4-7: kappa S q to columns 64 .. 127
+      const int part = warp >> 2;
+      const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32], o[16];
+        tmem_ld32(lane_base + (uint32_t)(kColS + 128 * part + 32 * c), v);
+        tmem_ld_wait();
+        const float inv = part ? 1.f / 16.f : A.g[TWO && c >= 2 ? 1 : 0].kinv;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = h2_bits(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+        tmem_st16(lane_base + (uint32_t)(kColQ + 64 * part + 16 * c), o);
+      }
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    ok = *abort_v == 0;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  ok = *abort_v == 0;
 
   if (warp < kSoftWarps) {
-    // ------------------------------------------------------------------ softmax, thread = row
-    const int r = threadIdx.x;
+    // ------------------------------------------------------------------ softmax, thread = lane = row of a copy
+    const int r = threadIdx.x % per;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
-    const bool warp_live = 32 * warp < live;
+    const bool warp_live = (32 * warp) % per < live;
     const int j = (r0 + r) / A.rep;
     const bool row_live = r < live;
-    const float sc = s_scale[r];
+    const float sc = s_scale[threadIdx.x];
     // columns of the tile at ts that the row attends (tiles past the context or the split's end)
     auto kept = [&](int ts) -> uint64_t {
       const uint64_t keep = t1 - ts < 64 ? (1ull << (t1 - ts)) - 1 : ~0ull;
@@ -495,32 +629,46 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const TreeArgs A
       return keep & bits;
     };
     float m = -INFINITY, l = 0.f;
+#pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
-      if (!wait_all(&bar->sfull[i & 1], (uint32_t)((i >> 1) & 1))) { fail(604); ok = false; break; }
+      const int st = i % kStages, ph = i / kStages;
+      if (!wait_all(&bar->sfull[st], ph)) { fail(604); ok = false; break; }
       tc_fence_after();
-      if (warp_live) {
-        const uint32_t col = lane_base + (uint32_t)(64 * (i & 1));
+      const uint32_t col = lane_base + (uint32_t)(kColS + 64 * st);
+      if (i % fold != (32 * warp) / per) {
+        // another copy's tile (a warp's lanes are of one copy)
+        uint32_t z[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = 0u;
+        tmem_st16(col, z);
+        tmem_st16(col + 16, z);
+        tmem_st_wait();
+        tc_fence_before();
+      } else if (warp_live) {
         const int ts = t0 + i * kTileTok;
-        const bool whole = ts + kTileTok <= min(ctx, t1);
-        const uint64_t keep = whole ? ~0ull : kept(ts);
-        // S is read twice, 32 columns at a time: for the maximum, then for the weights (64 values
-        // held at once would spill)
-        float mt = -INFINITY;
+        if (ts + kTileTok > min(ctx, t1)) {          // a last tile: columns that the row does not attend become -inf
+          uint64_t keep = kept(ts);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c, keep >>= 16) {
+            uint32_t s[16];
+            tmem_ld16(col + 16 * c, s);
+            tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t s[32];
-          tmem_ld32(col + 32 * k, s);
-          tmem_ld_wait();
-          if (whole) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) mt = fmaxf(mt, __uint_as_float(s[c]));
-          } else {
-            const uint32_t kk = (uint32_t)(keep >> (32 * k));
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if ((kk >> c) & 1) mt = fmaxf(mt, __uint_as_float(s[c]));
+            for (int e = 0; e < 16; ++e) s[e] = (keep >> e) & 1 ? s[e] : 0xFF800000u;
+            tmem_st16(col + 16 * c, s);
           }
+          tmem_st_wait();
         }
+        uint32_t s[64];
+        tmem_ld32(col, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+        tmem_ld32(col + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+        tmem_ld_wait();
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+        float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         mt = mt == -INFINITY ? mt : mt * sc;
         const bool first = m == -INFINITY;
         const bool grow = mt > m + kGrow;
@@ -531,10 +679,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const TreeArgs A
           l *= f;
         }
         if (i > 0 && __any_sync(0xffffffffu, grow && !first)) {
-          // O rows times f, once the products of the tile before are in
-          if (!wait_all(&bar->vempty, (uint32_t)((i - 1) & 1))) { fail(605); ok = false; break; }
+          // O rows times f, once the products of the tile before are in (S of tile i - 1 says that those of
+          // tile i - 5 are, so the parity is that of tile i - 1)
+          if (!wait_all(&bar->vempty[(i - 1) % kStages], (i - 1) / kStages)) { fail(605); ok = false; break; }
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
             tmem_ld16(lane_base + kColO + 16 * c, o);
@@ -544,35 +693,60 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const TreeArgs A
             tmem_st16(lane_base + kColO + 16 * c, o);
           }
         }
-        const float base = (m == -INFINITY ? 0.f : m) - kPShift;
+        const float base = kPShift - (m == -INFINITY ? 0.f : m);
+        const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t s[32], p[16];
-          tmem_ld32(col + 32 * k, s);
-          tmem_ld_wait();
-          const uint32_t kk = (uint32_t)(keep >> (32 * k));
+          uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float a = ex2(fmaf(__uint_as_float(s[2 * e]), sc, -base)), z = ex2(fmaf(__uint_as_float(s[2 * e + 1]), sc, -base));
-            if (!whole) {
-              a = (kk >> (2 * e)) & 1 ? a : 0.f;
-              z = (kk >> (2 * e + 1)) & 1 ? z : 0.f;
-            }
-            l += a + z;
-            p[e] = h2_bits(a, z);
+            const int c = 32 * k + 2 * e;
+            float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, base2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            sum = add2(sum, x);
+            p[e] = h2_bits(x.x, x.y);
           }
           tmem_st16(col + 16 * k, p);
         }
+        l += sum.x + sum.y;
         tmem_st_wait();
         tc_fence_before();
       }
-      mbar_arrive(&bar->pfull[i & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->pfull[st]);
     }
-    if (ok && !wait_all(&bar->vempty, (uint32_t)((n - 1) & 1))) { fail(606); ok = false; }
+    // the products of the last tiles (as above, the S of a tile says that those four tiles before it are in)
+#pragma unroll 1
+    for (int i = max(0, n - kStages); ok && i < n; ++i)
+      if (!wait_all(&bar->vempty[i % kStages], i / kStages)) { fail(606); ok = false; }
+    // weights of the copies: their common maximum and sum
+    if (fold > 1) {
+      s_ml[threadIdx.x] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->xfull);
+      if (ok && !wait_all(&bar->xfull, 0)) { fail(613); ok = false; }
+    }
+    float L = l, w = 1.f;
+    if (fold > 1) {
+      float M = -INFINITY;
+#pragma unroll 1
+      for (int c = r; c < kRows; c += per) M = fmaxf(M, s_ml[c].x);
+      L = 0.f;
+#pragma unroll 1
+      for (int c = r; c < kRows; c += per) {
+        const float2 x = s_ml[c];
+        if (x.x != -INFINITY) L += ex2(x.x - M) * x.y;
+        else L += x.y;                               // 0, or the NaN of a row without a maximum
+      }
+      w = m == -INFINITY ? 0.f : ex2(m - M);
+      m = M;
+    }
     if (ok) {
       tc_fence_after();
       if (warp_live) {
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const float inv = L > 0.f || L != L ? w / L : 0.f;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32], x[16];
@@ -580,129 +754,135 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const TreeArgs A
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = h2_bits(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          tmem_st16(lane_base + 16 * c, x);
+          tmem_st16(lane_base + kColS + 16 * c, x);
         }
         tmem_st_wait();
       }
       tc_fence_before();
-      mbar_arrive(&bar->ofull);
-      if (!wait_all(&bar->dfull, 0)) { fail(607); ok = false; }
     }
-    if (ok) {
-      tc_fence_after();
-      const size_t row = (size_t)bh * A.R + r0 + r;
-      const size_t qr = r < nrow ? q_row(A, b, hk, r0 + r) * kTD : 0;
-      if (warp_live) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar->ofull);
+    if (ok && !wait_all(&bar->dfull, 0)) { fail(607); ok = false; }
+    tc_fence_after();
+    // the rotated rows of every copy to shared memory
+    float* sums = reinterpret_cast<float*>(smem + kOffSum) + threadIdx.x * kSumLd;
+    if (ok && warp_live) {
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[16];
-          tmem_ld16(lane_base + kColO + 16 * c, o);
-          tmem_ld_wait();
-          const float inv16 = row_live ? 1.f / 16.f : 0.f;
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld16(lane_base + kColO + 16 * c, o);
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            float4 v = make_float4(__uint_as_float(o[e]) * inv16, __uint_as_float(o[e + 1]) * inv16,
-                                   __uint_as_float(o[e + 2]) * inv16, __uint_as_float(o[e + 3]) * inv16);
-            if (!row_live) v = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int ch = 16 * c + e;
-            if (r >= nrow) {
-            } else if (A.nsplit > 1) {
-              *reinterpret_cast<float4*>(A.part + (row * A.nsplit + split) * kTD + ch) = v;
-            } else if (A.perm) {
-              const int4 to = __ldg(reinterpret_cast<const int4*>(A.perm + (size_t)hk * kTD + ch));
-              if (to.x >= 0 && to.x < kTD) store_any(A.out, A.q_dtype, qr + to.x, v.x);
-              if (to.y >= 0 && to.y < kTD) store_any(A.out, A.q_dtype, qr + to.y, v.y);
-              if (to.z >= 0 && to.z < kTD) store_any(A.out, A.q_dtype, qr + to.z, v.z);
-              if (to.w >= 0 && to.w < kTD) store_any(A.out, A.q_dtype, qr + to.w, v.w);
-            } else {
-              store_any4(A.out, A.q_dtype, qr + ch, v);
-            }
-          }
-        }
-      } else if (r < nrow && A.nsplit == 1) {
-        for (int e = 0; e < kTD; e += 4) store_any4(A.out, A.q_dtype, qr + e, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<uint4*>(sums + 16 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
-      if (A.nsplit > 1 && r < nrow) A.ml[row * A.nsplit + split] = make_float2(m - kPShift, row_live ? l : 0.f);
     }
-  } else if (warp < kSoftWarps + kDecWarps) {
+    if (A.nsplit > 1 && threadIdx.x < nrow)
+      A.ml[((size_t)bh * A.R + r0 + threadIdx.x) * A.nsplit + split] = make_float2(m - kPShift, row_live ? L : 0.f);
+  } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------------ decoders
-    const int dw = warp - kSoftWarps, half = dw >> 1, row = 32 * (dw & 1) + lane;
     int code = 0;
     if (ok) {
-      if (half == 0) ok = decode_loop<PK0, PV0, TWO>(A, A.g[0], smem, bar, 0, row, b, hk, t0, t1, n, abort_v, code);
-      else ok = decode_loop<PK1, PV1, TWO>(A, A.g[TWO ? 1 : 0], smem, bar, 1, row, b, hk, t0, t1, n, abort_v, code);
+      if (!TWO || half == 0)
+        ok = Decode<PK0, PV0, TWO>::loop(dec, A, A.g[0], smem, bar, half, set, drow, b, hk, t1, n, abort_v, code);
+      else
+        ok = Decode<PK1, PV1, TWO>::loop(dec, A, A.g[1], smem, bar, 1, set, drow, b, hk, t1, n, abort_v, code);
       if (!ok) fail(code);
     }
-    // the value rotation into the K buffer, once the last logits are formed
-    if (ok && !wait(&bar->kempty, (uint32_t)((n - 1) & 1))) { fail(608); ok = false; }
+    // the value rotation into the first K stage, once the last logits are formed
+    if (ok && !wait_all(&bar->klast, 0)) { fail(608); ok = false; }
     if (ok) {
-      const int t = threadIdx.x - kSoft;
-      copy_matrix(smem + kOffK, A.g[0].piv, TWO ? 64 : 128, TWO ? 64 : 128, t, kDec);
-      if (TWO) copy_matrix(smem + kOffK + 8192, A.g[1].piv, 64, 64, t, kDec);
+      const int t = threadIdx.x - 32 * kSoftWarps;
+      copy_matrix<TWO ? 64 : 128>(smem, A.g[0].piv, t, 32 * kDecWarps);
+      if (TWO) copy_matrix<64>(smem + 8192, A.g[1].piv, t, 32 * kDecWarps);
+      copy_wait();
       fence_proxy_async_smem();
-      mbar_arrive(&bar->wfull);
     }
-  } else if (lane == 0) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar->wfull);
+  } else {
     // ------------------------------------------------------------------ products
-    const uint32_t qa = smem_u32(smem), ka = smem_u32(smem + kOffK), va = smem_u32(smem + kOffV);
-    const uint32_t id_s = idesc_f16(kRows, kTileTok, 0), id_o = idesc_f16(kRows, kTD, 0) | kMajorN;
-    for (int i = 0; ok && i <= n; ++i) {
+    const uint32_t k0 = smem_u32(smem), v0 = smem_u32(smem + kOffV);
+    constexpr uint32_t id_s = idesc_f16(kRows, kTileTok, 0), id_o = idesc_f16(kRows, kTD, 0) | kMajorN;
+#pragma unroll 1
+    for (int i = 0; ok && i < n + kAhead; ++i) {
       if (i < n) {
-        if (!wait(&bar->kfull, (uint32_t)(i & 1))) { fail(609); ok = false; break; }
-        // S(i) takes the columns of P(i - 2): its products are in
-        if (i >= 2 && !wait(&bar->vempty, (uint32_t)(i & 1))) { fail(610); ok = false; break; }
+        const int st = i % kStages, ph = i / kStages;
+        // S takes the columns of P of four tiles before: its products are in
+        if (!wait_all(&bar->kfull[st], ph)) { fail(609); ok = false; break; }
+        if (!wait_all(&bar->vempty[st], ph + 1)) { fail(610); ok = false; break; }
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(64 * (i & 1));
+        const uint32_t kb = k0 + st * kKBytes, d = tmem + (uint32_t)(kColS + 64 * st);
+#pragma unroll 4
         for (int k = 0; k < 16; ++k)
-          mma_ss(d, desc_sw128(qa + (k >> 2) * (kRows * 128) + (k & 3) * 32),
-                 desc_sw128(ka + (k >> 2) * (kTileTok * 128) + (k & 3) * 32), id_s, k ? 1u : 0u);
-        mma_commit(&bar->sfull[i & 1]);
-        mma_commit(&bar->kempty);
+          mma_ts_warp(d, tmem + (uint32_t)(kColQ + 8 * k), desc_sw128(kb + (k >> 2) * (kTileTok * 128) + (k & 3) * 32), id_s, k ? 1u : 0u);
+        mma_commit_warp(&bar->sfull[st]);
+        mma_commit_warp(&bar->kempty[st]);
+        if (i == n - 1) mma_commit_warp(&bar->klast);
       }
-      if (i > 0) {
-        const int p = i - 1;
-        if (!wait(&bar->pfull[p & 1], (uint32_t)((p >> 1) & 1)) || !wait(&bar->vfull, (uint32_t)(p & 1))) {
-          fail(611);
-          ok = false;
-          break;
-        }
+      if (i >= kAhead) {
+        const int p = i - kAhead, st = p % kStages, ph = p / kStages;
+        if (!wait_all(&bar->vfull[st], ph) || !wait_all(&bar->pfull[st], ph)) { fail(611); ok = false; break; }
         tc_fence_after();
+        const uint32_t vb = v0 + st * kVBytes, a = tmem + (uint32_t)(kColS + 64 * st);
+#pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ts(tmem + kColO, tmem + (uint32_t)(64 * (p & 1) + 8 * k), desc_mn(va + k * 2048, kTileTok * 128), id_o,
-                 p > 0 || k > 0 ? 1u : 0u);
-        mma_commit(&bar->vempty);
+          mma_ts_warp(tmem + kColO, a + (uint32_t)(8 * k), desc_mn(vb + k * 2048, kTileTok * 128), id_o, p > 0 || k > 0 ? 1u : 0u);
+        mma_commit_warp(&bar->vempty[st]);
       }
     }
-    if (ok && (!wait(&bar->wfull, 0) || !wait(&bar->ofull, 0))) { fail(612); ok = false; }
+    if (ok && (!wait_all(&bar->wfull, 0) || !wait_all(&bar->ofull, 0))) { fail(612); ok = false; }
     if (ok) {
       // out = O / l times Pi of the values
       tc_fence_after();
+      const uint32_t a = tmem + kColS;
       if (TWO) {
-        const uint32_t id = idesc_f16(kRows, 64, 0);
+        constexpr uint32_t id = idesc_f16(kRows, 64, 0);
         for (int g = 0; g < 2; ++g)
           for (int k = 0; k < 4; ++k)
-            mma_ts(tmem + kColO + 64 * g, tmem + (uint32_t)(32 * g + 8 * k), desc_sw128(ka + g * 8192 + k * 32), id, k ? 1u : 0u);
+            mma_ts_warp(tmem + kColO + 64 * g, a + (uint32_t)(32 * g + 8 * k), desc_sw128(k0 + g * 8192 + k * 32), id, k ? 1u : 0u);
       } else {
-        const uint32_t id = idesc_f16(kRows, kTD, 0);
+        constexpr uint32_t id = idesc_f16(kRows, kTD, 0);
         for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + kColO, tmem + (uint32_t)(8 * k), desc_sw128(ka + (k >> 2) * (kTD * 128) + (k & 3) * 32), id, k ? 1u : 0u);
+          mma_ts_warp(tmem + kColO, a + (uint32_t)(8 * k), desc_sw128(k0 + (k >> 2) * (kTD * 128) + (k & 3) * 32), id, k ? 1u : 0u);
       }
-      mma_commit(&bar->dfull);
+      mma_commit_warp(&bar->dfull);
     }
-    mma_commit(&bar->drain);
+    mma_commit_warp(&bar->drain);
     mbar_wait(&bar->drain, 0, nullptr, kDrainNs);
+    __syncwarp();
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftWarps + kDecWarps) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if (*abort_v) return;
+  // ------------------------------------------------------------------ the copies' sum, a warp a row
+  const float inv = A.g[TWO && lane >= 16 ? 1 : 0].vinv;
+#pragma unroll 1
+  for (int r = warp; r < nrow; r += kThreads / 32) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < live) {
+#pragma unroll 1
+      for (int c = r; c < kRows; c += per) {
+        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + kOffSum) + c * kSumLd + 4 * lane);
+        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+      }
+      v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    }
+    if (A.nsplit > 1)
+      *reinterpret_cast<float4*>(A.part + (((size_t)bh * A.R + r0 + r) * A.nsplit + split) * kTD + 4 * lane) = v;
+    else
+      store_row<T>(static_cast<T*>(A.out) + q_row(A, b, hk, r0 + r) * kTD, perm, lane, v);
   }
 }
 
 // Log-sum-exp merge of the splits, one warp per row, lane = 4 channels.
-__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs A) {
+template <typename T>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs A) {
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= (int64_t)A.B * A.Hkv * A.R) return;
   const int lane = threadIdx.x & 31;
@@ -733,16 +913,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs A) {
   }
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
   a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-  const size_t base = q_row(A, b, hk, r) * kTD;
-  if (A.perm) {
-    const int4 to = __ldg(reinterpret_cast<const int4*>(A.perm + (size_t)hk * kTD) + lane);
-    if (to.x >= 0 && to.x < kTD) store_any(A.out, A.q_dtype, base + to.x, a.x);
-    if (to.y >= 0 && to.y < kTD) store_any(A.out, A.q_dtype, base + to.y, a.y);
-    if (to.z >= 0 && to.z < kTD) store_any(A.out, A.q_dtype, base + to.z, a.z);
-    if (to.w >= 0 && to.w < kTD) store_any(A.out, A.q_dtype, base + to.w, a.w);
-  } else {
-    store_any4(A.out, A.q_dtype, base + 4 * lane, a);
-  }
+  store_row<T>(static_cast<T*>(A.out) + q_row(A, b, hk, r) * kTD, A.perm ? A.perm + (size_t)hk * kTD : nullptr, lane, a);
 }
 
 struct TreeWs {
@@ -750,7 +921,7 @@ struct TreeWs {
   int nsplit, chunk;
 };
 
-// Splits of the tokens: as many as give the shortest modelled time, waves of CTAs (two per SM)
+// Splits of the tokens: as many as give the shortest modelled time, waves of CTAs (one per SM)
 // times (tiles per CTA + the cost of a CTA's start and end, about kEdge tiles).
 constexpr int kEdge = 8, kMaxSplit = 128;
 
@@ -769,7 +940,7 @@ TreeWs tree_ws(int B, int T, int Hq, int Hkv, int64_t max_len) {
   for (int64_t s = 1; s <= std::min<int64_t>(kMaxSplit, tiles); ++s) {
     const int64_t per = (tiles + s - 1) / s;
     if (s > 1 && (tiles + per - 1) / per < s) continue;        // same split as a smaller s
-    const double t = (double)((std::max<int64_t>(1, ctas) * s + 2 * sms - 1) / (2 * sms)) * (double)(per + kEdge);
+    const double t = (double)((std::max<int64_t>(1, ctas) * s + sms - 1) / sms) * (double)(per + kEdge);
     if (t < best_t - 1e-9) {
       best_t = t;
       best = s;
@@ -784,13 +955,27 @@ TreeWs tree_ws(int B, int T, int Hq, int Hkv, int64_t max_len) {
   return w;
 }
 
-template <int PK0, int PV0, int PK1, int PV1, bool TWO>
+template <int PK0, int PV0, int PK1, int PV1, bool TWO, typename T>
 int launch_main(const TreeArgs& A, unsigned ctas, cudaStream_t st) {
-  cudaError_t e = ensure_smem_attrs<tree_attn_kernel<PK0, PV0, PK1, PV1, TWO>>(kSmem, true);
+  cudaError_t e = ensure_smem_attrs<tree_attn_kernel<PK0, PV0, PK1, PV1, TWO, T>>(kSmem, true);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tree_attn_kernel)");
-  tree_attn_kernel<PK0, PV0, PK1, PV1, TWO><<<ctas, kThreads, kSmem, st>>>(A);
+  tree_attn_kernel<PK0, PV0, PK1, PV1, TWO, T><<<ctas, kThreads, kSmem, st>>>(A);
   count_launch();
   return check_launch("tree_attn_kernel");
+}
+
+template <typename T>
+int launch_typed(const TreeArgs& A, int G, int key_bits, cudaStream_t st) {
+  const unsigned ctas = (unsigned)((int64_t)A.B * A.Hkv * A.tiles_r * A.nsplit);
+  int r;
+  if (G == 1 && key_bits == 4) r = launch_main<4, 4, 4, 4, false, T>(A, ctas, st);
+  else if (G == 1) r = launch_main<3, 3, 3, 3, false, T>(A, ctas, st);
+  else if (key_bits == 4) r = launch_main<4, 4, 3, 3, true, T>(A, ctas, st);
+  else r = launch_main<3, 3, 2, 2, true, T>(A, ctas, st);
+  if (r != TQ_OK || A.nsplit == 1) return r;
+  tree_merge_kernel<T><<<(unsigned)(((int64_t)A.B * A.Hkv * A.R + 7) / 8), 256, 0, st>>>(A);
+  count_launch();
+  return check_launch("tree_merge_kernel");
 }
 
 uint32_t half_bits(float v) {
@@ -813,16 +998,17 @@ int launch_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, 
   TreeArgs A{};
   A.B = B; A.T = T; A.Hq = Hq; A.Hkv = Hkv; A.rep = Hq / Hkv; A.R = T * A.rep;
   A.tiles_r = (A.R + kRows - 1) / kRows;
+  A.fold = A.R <= kRows / 4 ? 4 : A.R <= kRows / 2 ? 2 : 1;
   A.nsplit = W.nsplit; A.chunk = W.chunk;
   A.words = (T + 63) / 64;
   A.max_len = max_len;
   A.scale_log2 = fabsf(scale) * 1.4426950408889634f;
   A.sign = scale < 0.f ? -1.f : 1.f;
-  A.q = q; A.q_dtype = q_dtype; A.out = out;
+  A.q = q; A.out = out;
   A.seq_lens = seq_lens; A.draft_lens = draft_lens; A.mask = mask; A.perm = perm; A.table = table;
   A.part = reinterpret_cast<float*>(ws);
   A.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + W.ml);
-  A.wait_ns = pipeline_wait_ns();
+  A.wait = 2 * pipeline_wait_ns();      // (1.965 GHz at most: a limit in ns is never cut short)
   A.err = kctx[0]->dev_err;
   int64_t pool = INT64_MAX;
   for (int g = 0; g < G; ++g) {
@@ -830,13 +1016,17 @@ int launch_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, 
     t.kcodes = kc[g].codes; t.knorm = kc[g].norm; t.krnorm = kc[g].rnorm; t.vcodes = vc[g].codes; t.vnorm = vc[g].norm;
     const Codebook &kb = kctx[g]->cb, &vb = vctx[g]->cb;
     for (int i = 0; i < kb.K && i < 8; ++i) {
-      t.klo[i / 4] |= (half_bits(kb.cc[i]) & 0xFF) << (8 * (i % 4));
-      t.khi[i / 4] |= (half_bits(kb.cc[i]) >> 8) << (8 * (i % 4));
+      const uint32_t h = half_bits(kb.cc[i] * kctx[g]->lev_scale);
+      t.klo[i / 4] |= (h & 0xFF) << (8 * (i % 4));
+      t.khi[i / 4] |= (h >> 8) << (8 * (i % 4));
     }
     for (int i = 0; i < vb.K / 2 && i < 8; ++i) {
-      t.vlo[i / 4] |= (half_bits(vb.c[vb.K / 2 + i]) & 0xFF) << (8 * (i % 4));
-      t.vhi[i / 4] |= (half_bits(vb.c[vb.K / 2 + i]) >> 8) << (8 * (i % 4));
+      const uint32_t h = half_bits(vb.c[vb.K / 2 + i] * vctx[g]->lev_scale);
+      t.vlo[i / 4] |= (h & 0xFF) << (8 * (i % 4));
+      t.vhi[i / 4] |= (h >> 8) << (8 * (i % 4));
     }
+    t.kinv = 1.f / (16.f * kctx[g]->lev_scale);
+    t.vinv = 1.f / (16.f * vctx[g]->lev_scale);
     t.pi = static_cast<const __half*>(kctx[g]->PiT_f16);
     t.st = static_cast<const __half*>(kctx[g]->ST_f16);
     t.piv = static_cast<const __half*>(vctx[g]->PiT_f16);
@@ -847,16 +1037,10 @@ int launch_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, 
     A.max_pages = (int)(max_len / page);
     A.npages = pool / ((int64_t)Hkv * page);
   }
-  const unsigned ctas = (unsigned)((int64_t)B * Hkv * A.tiles_r * A.nsplit);
-  int r;
-  if (G == 1 && kctx[0]->lay.planes == 4) r = launch_main<4, 4, 4, 4, false>(A, ctas, st);
-  else if (G == 1) r = launch_main<3, 3, 3, 3, false>(A, ctas, st);
-  else if (kctx[0]->lay.planes == 4) r = launch_main<4, 4, 3, 3, true>(A, ctas, st);
-  else r = launch_main<3, 3, 2, 2, true>(A, ctas, st);
-  if (r != TQ_OK || A.nsplit == 1) return r;
-  tree_merge_kernel<<<(unsigned)(((int64_t)B * Hkv * A.R + 7) / 8), 256, 0, st>>>(A);
-  count_launch();
-  return check_launch("tree_merge_kernel");
+  const int key_bits = kctx[0]->lay.planes;
+  if (q_dtype == TQ_DTYPE_F32) return launch_typed<float>(A, G, key_bits, st);
+  if (q_dtype == TQ_DTYPE_BF16) return launch_typed<__nv_bfloat16>(A, G, key_bits, st);
+  return launch_typed<__half>(A, G, key_bits, st);
 }
 
 }  // namespace tq

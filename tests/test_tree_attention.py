@@ -136,6 +136,15 @@ def test_tree_long_context_in_many_splits():
 
 
 @gpu
+@pytest.mark.parametrize("T", [2, 5, 9, 17])
+@pytest.mark.parametrize("kind", ["4", "2.5"])
+def test_tree_many_tiles_a_block(T, kind):
+    """So many kv heads that a block runs through 1 to 11 tiles: every phase of its pipeline, in each fold of the rows."""
+    lens = [64 * i + (i % 3) for i in range(1, 12)]
+    _case(16, kind, 4 * 16, 16, T, lens, [T] * 11, page=64)
+
+
+@gpu
 def test_tree_odd_cache_lengths():
     """Sequences start at odd slots, so records and norms sit at odd offsets."""
     _case(4, "3.5", 12, 3, 5, [257, 130], [5, 5], max_len=257)
