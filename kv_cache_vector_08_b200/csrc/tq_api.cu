@@ -748,6 +748,9 @@ int tq_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, cons
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(perm, 16) || !aligned(tree_mask, 8))
     return fail(TQ_ERR_UNSUPPORTED, "q, out and the channel permutation must be 16-byte aligned, the mask 8-byte aligned");
   if (!decode_caches_supported(kctx, vctx, ngroups, kcache, vcache)) return unsupported_caches("tq_tree_attention");
+  for (int g = 0; g < ngroups; ++g)
+    if (kcache[g].cap > INT32_MAX || vcache[g].cap > INT32_MAX)
+      return fail(TQ_ERR_UNSUPPORTED, "tq_tree_attention: a cache of more than 2^31 - 1 slots");
   const size_t need = tree_workspace_bytes(B, T, Hq, Hkv, max_len);
   if (!workspace || ws_bytes < need) return fail(TQ_ERR_WORKSPACE, "workspace too small");
   if (!aligned(workspace, 16)) return fail(TQ_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");

@@ -17,7 +17,7 @@
 // memory as the A operand, because a product that fetches both operands from shared memory is
 // bound by that at 64 columns (measured: 768 cycles of a tile's S instead of 256).  Then a pipeline
 // of tiles, four deep in K, V and S:
-//   decoders (8 warps, two sets that take alternate tiles; thread = token x half of the head): code
+//   decoders (12 warps, three sets that take every third tile; thread = token x half of the head): code
 //     words come from global memory a tile ahead, byte-permute lookups make fp16 levels; K is
 //     written K-major, V with the channels contiguous, as it lies in the cache;
 //   products (one warp): S of tile i, then O += P V of tile i - 2;
@@ -25,10 +25,10 @@
 //     that moves only when it grew by 2^8, so that O, which stays in tensor memory, is seldom
 //     rescaled.
 // Rows that fill a half or a quarter of the 128 lanes are repeated in the others (fold 2 or 4), and
-// each copy takes every second or fourth tile: the lanes of the other copies put zeros into its P.
-// The products cost the same, the exponentials spread over all lanes.  The copies' sums meet at the
-// end.  At last O / l is rotated back by one more product, and written (one split) or left as a
-// partial for the merge kernel.
+// each copy takes its half or quarter of the tile's columns, with zeros in the rest of its P.  The
+// products cost the same, the exponentials spread over all lanes.  The copies' sums meet at the end.
+// At last O / l is rotated back by one more product, and written (one split) or left as a partial
+// for the merge kernel.
 //
 // The levels of a codebook enter scaled by a factor for which fp16 holds them almost exactly
 // (tq_init looks for it); the projection and the last product take the factor out.
@@ -56,9 +56,9 @@ using mmaops::prmt;
 constexpr int kTD = 128;          // head dimension
 constexpr int kTileTok = 64;      // tokens per tile: a tile never crosses a page
 constexpr int kRows = 128;        // query rows per CTA
-constexpr int kSoftWarps = 4, kDecWarps = 8, kMmaWarp = kSoftWarps + kDecWarps;
+constexpr int kSoftWarps = 4, kDecWarps = 12, kMmaWarp = kSoftWarps + kDecWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kDecSet = kDecWarps / 2;      // warps that decode one tile
+constexpr int kDecSet = 4, kSets = kDecWarps / kDecSet;   // warps that decode one tile, sets of them
 constexpr int kStages = 4;                  // tiles in flight (K, V, S)
 constexpr int kAhead = 2;                   // S runs this many tiles ahead of O += P V
 constexpr uint64_t kDrainNs = 2000000000ull;
@@ -91,7 +91,7 @@ struct TreeGroup {
 struct TreeArgs {
   TreeGroup g[2];
   int B, T, Hq, Hkv, rep, R, fold, tiles_r, nsplit, chunk, words;
-  int64_t max_len, npages;
+  int max_len, npages;
   float scale_log2;               // |scale| log2(e)
   float sign;                     // sign of the scale
   const void* q;
@@ -100,6 +100,7 @@ struct TreeArgs {
   const uint64_t* mask;
   const int32_t *perm, *table;
   int page, max_pages;
+  uint32_t page_inv;              // 2^32 / page, rounded down
   float* part;                    // [B Hkv R][nsplit][128] rotated partial results
   float2* ml;                     // [B Hkv R][nsplit] (maximum in log2, sum)
   uint64_t wait;                  // limit of a wait, in SM cycles
@@ -188,7 +189,7 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
 
 // Tokens of sequence b and the drafted ones among them.
 __device__ __forceinline__ void lens_of(const TreeArgs& A, int b, int& len, int& nd) {
-  len = (int)max((int64_t)0, min((int64_t)A.seq_lens[b], A.max_len));
+  len = max(0, min(A.seq_lens[b], A.max_len));
   nd = min(len, A.T);
   if (A.draft_lens) nd = max(0, min(nd, A.draft_lens[b]));
 }
@@ -245,9 +246,10 @@ __device__ __forceinline__ uint2 ld_ahead8(const void* p) {
   asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint16_t ld_ahead2(const void* p) {
-  uint16_t v;
-  asm volatile("ld.global.nc.u16 %0, [%1];\n" : "=h"(v) : "l"(p));
+// (into a 32-bit register: widening a 16-bit one would wait for the load on the spot)
+__device__ __forceinline__ uint32_t ld_ahead2(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];\n" : "=r"(v) : "l"(p));
   return v;
 }
 template <int P>
@@ -345,18 +347,27 @@ __device__ __forceinline__ void decode_values(const uint32_t (&x)[8], const Tree
   }
 }
 
+// The same for two barriers, looked at in one go.
+__device__ __forceinline__ bool bar_wait2(uint64_t* a, int pa, uint64_t* b, int pb, const volatile int* abort, uint64_t limit) {
+  const bool ra = mbar_try_wait(a, (uint32_t)pa & 1u), rb = mbar_try_wait(b, (uint32_t)pb & 1u);
+  return __all_sync(0xffffffffu, (ra && rb) || (bar_wait(a, pa, abort, limit) && bar_wait(b, pb, abort, limit))) != 0;
+}
+
 struct Bars {
   uint64_t proj, klast, wfull, xfull, ofull, dfull, drain;
-  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages], sfull[kStages], pfull[kStages];
+  // of a stage: K decoded, S formed (so K is free), V decoded, O += P V done (so V and P are free), P formed
+  uint64_t kfull[kStages], sfull[kStages], vfull[kStages], vempty[kStages], pfull[kStages];
 };
 
-// One decoder thread: token `row` and one half of the head, of tiles set, set + 2, ...  Its code
+// One decoder thread: token `row` and one half of the head, of tiles set, set + 3, ...  Its code
 // words and norms of the next tile come from memory while it decodes this one.
 struct Decoder {
   uint32_t kw[8], vw[8];
-  uint16_t kn, kr, vn;
-  int64_t slot;                 // of the next tile's token, -1 past the end
-  int tok, pi, po, pg;          // the token after that: page entry, offset, page
+  uint32_t kn, kr, vn;
+  uint32_t slot;                // of the next tile's token; past the end, of any token of the sequence
+  bool live;                    // not past the end (else the token's norms count as 0; nothing here depends on a
+                                // loaded value before the tile is decoded, which would wait for the load)
+  int tok, po, pg;              // the token after that: offset in its page, page
 };
 
 template <int PK, int PV, bool TWO>
@@ -366,57 +377,46 @@ struct Decode {
   static constexpr int kPart = TWO ? 0 : PK * 8, vPart = TWO ? 0 : PV * 8;
 
   __device__ static __forceinline__ void load_k(Decoder& x, const TreeGroup& g, int half) {
-    x.kn = x.kr = 0;
-#pragma unroll
-    for (int i = 0; i < 2 * PK; ++i) x.kw[i] = 0u;
-    if (x.slot >= 0) {
-      load_words<PK>(x.kw, g.kcodes + x.slot * kRec + half * kPart);
-      x.kn = ld_ahead2(g.knorm + x.slot);
-      x.kr = ld_ahead2(g.krnorm + x.slot);
-    }
+    load_words<PK>(x.kw, g.kcodes + (uint64_t)x.slot * kRec + half * kPart);
+    x.kn = ld_ahead2(g.knorm + x.slot);
+    x.kr = ld_ahead2(g.krnorm + x.slot);
   }
   __device__ static __forceinline__ void load_v(Decoder& x, const TreeGroup& g, int half) {
-    x.vn = 0;
-#pragma unroll
-    for (int i = 0; i < 2 * PV; ++i) x.vw[i] = 0u;
-    if (x.slot >= 0) {
-      load_words<PV>(x.vw, g.vcodes + x.slot * vRec + half * vPart);
-      x.vn = ld_ahead2(g.vnorm + x.slot);
-    }
+    load_words<PV>(x.vw, g.vcodes + (uint64_t)x.slot * vRec + half * vPart);
+    x.vn = ld_ahead2(g.vnorm + x.slot);
   }
-  // Slot of the token, two tiles further with every call; the page entry of a call is loaded by
-  // the call before.
+  // Page entry and offset of token x.tok.
+  __device__ static __forceinline__ void locate(Decoder& x, const TreeArgs& A, int b) {
+    if (!A.table) return;
+    int pi = (int)__umulhi((uint32_t)x.tok, A.page_inv);      // x.tok / page, or one less
+    x.po = x.tok - pi * A.page;
+    if (x.po >= A.page) { x.po -= A.page; ++pi; }
+    x.pg = __ldg(A.table + (size_t)b * A.max_pages + pi);
+  }
+  // Slot of token x.tok, and on to the set's next token; the page entry of a call is loaded by the
+  // call before.
   __device__ static __forceinline__ void advance(Decoder& x, const TreeArgs& A, int b, int hk, int t1) {
-    if (x.tok >= t1) {
-      x.slot = -1;
-      return;
+    x.live = x.tok < t1;
+    if (!x.live) return;
+    if (A.table) {
+      if ((unsigned)x.pg >= (unsigned)A.npages) {
+        if (A.err) atomicCAS(A.err, 0, (int)kErrSlotRange);
+        x.pg = 0;
+      }
+      x.slot = (uint32_t)((x.pg * A.Hkv + hk) * A.page + x.po);
+    } else {
+      x.slot = (uint32_t)((b * A.Hkv + hk) * A.max_len + x.tok);
     }
-    if (!A.table) {
-      x.slot = ((int64_t)b * A.Hkv + hk) * A.max_len + x.tok;
-      x.tok += 2 * kTileTok;
-      return;
-    }
-    if (x.pg < 0 || x.pg >= A.npages) {
-      if (A.err) atomicCAS(A.err, 0, (int)kErrSlotRange);
-      x.pg = 0;
-    }
-    x.slot = ((int64_t)x.pg * A.Hkv + hk) * A.page + x.po;
-    x.tok += 2 * kTileTok;
-    if (x.tok < t1) {
-      const int was = x.pi;
-      x.po += 2 * kTileTok;
-#pragma unroll 1
-      while (x.po >= A.page) { x.po -= A.page; ++x.pi; }
-      if (x.pi != was) x.pg = __ldg(A.table + (size_t)b * A.max_pages + x.pi);
-    }
+    x.tok += kSets * kTileTok;
+    if (x.tok < t1) locate(x, A, b);
   }
   __device__ static __forceinline__ void start(Decoder& x, const TreeArgs& A, const TreeGroup& g, int half, int tok, int b,
                                                int hk, int t1) {
-    x.tok = tok;
-    x.pi = A.table ? tok / A.page : 0;
-    x.po = A.table ? tok - x.pi * A.page : 0;
-    x.pg = A.table && tok < t1 ? __ldg(A.table + (size_t)b * A.max_pages + x.pi) : 0;
+    x.tok = min(tok, t1 - 1);
+    x.po = x.pg = 0;
+    locate(x, A, b);
     advance(x, A, b, hk, t1);
+    x.live = tok < t1;
     load_k(x, g, half);
     load_v(x, g, half);
   }
@@ -428,20 +428,21 @@ struct Decode {
     auto wait = [&](uint64_t* p, int parity) {
       return __all_sync(0xffffffffu, bar_wait(p, parity, abort_v, A.wait)) != 0;
     };
-    auto f = [](uint16_t h) { return __half2float(__ushort_as_half(h)); };
+    auto f = [](uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); };
 #pragma unroll 1
-    for (int i = set; i < n; i += 2) {
+    for (int i = set; i < n; i += kSets) {
       const int st = i % kStages, ph = i / kStages;
+      const bool live = x.live;
       advance(x, A, b, hk, t1);
-      if (!wait(&bar->kempty[st], ph + 1)) { code = 601; return false; }
+      if (!wait(&bar->sfull[st], ph + 1)) { code = 601; return false; }
       uint8_t* lev = smem + st * kKBytes + part;
-      decode_keys<PK>(x.kw, g, f(x.kn), f(x.kr), lev, lev + 2 * (kTileTok * 128), row);
+      decode_keys<PK>(x.kw, g, live ? f(x.kn) : 0.f, live ? f(x.kr) : 0.f, lev, lev + 2 * (kTileTok * 128), row);
       load_k(x, g, half);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane0) mbar_arrive(&bar->kfull[st]);
       if (!wait(&bar->vempty[st], ph + 1)) { code = 602; return false; }
-      decode_values<PV>(x.vw, g, f(x.vn), smem + kOffV + st * kVBytes + part, row);
+      decode_values<PV>(x.vw, g, live ? f(x.vn) : 0.f, smem + kOffV + st * kVBytes + part, row);
       load_v(x, g, half);
       fence_proxy_async_smem();
       __syncwarp();
@@ -459,7 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   float* s_scale = reinterpret_cast<float*>(smem + kOffMisc + 512);      // [128] logit scale of a lane's row
   float2* s_ml = reinterpret_cast<float2*>(smem + kOffMisc + 1024);      // [128] the copies' maxima and sums
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a shuffle makes the warp's number, and what the products' addresses come from, known to be uniform: the
+  // compiler then keeps the operands of the products in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int split = blockIdx.x % A.nsplit;
   const int rt = (blockIdx.x / A.nsplit) % A.tiles_r;
   const int bh = blockIdx.x / (A.nsplit * A.tiles_r), b = bh / A.Hkv, hk = bh % A.Hkv;
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         store_row<T>(static_cast<T*>(A.out) + q_row(A, b, hk, r0 + r) * kTD, nullptr, lane, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
-  const int n = (t1 - t0 + kTileTok - 1) / kTileTok;
+  const int n = __shfl_sync(0xffffffffu, (t1 - t0 + kTileTok - 1) / kTileTok, 0);
   const int fold = A.fold, per = kRows / fold;           // copies of the rows, lanes of a copy
   if (threadIdx.x == 0) {
     mbar_init(&bar->proj, 1);
@@ -486,7 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar->kfull[i], kDecSet);
-      mbar_init(&bar->kempty[i], 1);
       mbar_init(&bar->vfull[i], kDecSet);
       mbar_init(&bar->vempty[i], 1);
       mbar_init(&bar->sfull[i], 1);
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    tmem = *tmem_slot;
+    tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     if (warp == kMmaWarp) {
       // D columns 64 j: coordinates 64 j .. of Pi q, then (from 128 on) of kappa S q
       constexpr uint32_t idesc = idesc_f16(kRows, 64, 0) | kMajorN;
@@ -628,47 +630,55 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       if (sh && w + 1 < A.words) bits |= __ldg(mr + w + 1) << (64 - sh);
       return keep & bits;
     };
+    const int copy = (32 * warp) / per, nch = 4 / fold, c0 = copy * 16 * nch;      // (a warp's lanes are of one copy)
+    // sixteen columns of S to eight of P
+    auto weights = [&](const uint32_t* s, float2 sc2, float2 base2, float2& sum, uint32_t (&p)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float2 x = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, base2);
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
+        sum = add2(sum, x);
+        p[e] = h2_bits(x.x, x.y);
+      }
+    };
     float m = -INFINITY, l = 0.f;
 #pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
       const int st = i % kStages, ph = i / kStages;
       if (!wait_all(&bar->sfull[st], ph)) { fail(604); ok = false; break; }
       tc_fence_after();
-      const uint32_t col = lane_base + (uint32_t)(kColS + 64 * st);
-      if (i % fold != (32 * warp) / per) {
-        // another copy's tile (a warp's lanes are of one copy)
-        uint32_t z[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) z[e] = 0u;
-        tmem_st16(col, z);
-        tmem_st16(col + 16, z);
-        tmem_st_wait();
-        tc_fence_before();
-      } else if (warp_live) {
+      if (warp_live) {
+        // this copy's columns, 16 at a time: c0 .. c0 + 16 nch
+        const uint32_t col = lane_base + (uint32_t)(kColS + 64 * st), sc0 = col + (uint32_t)c0;
         const int ts = t0 + i * kTileTok;
         if (ts + kTileTok > min(ctx, t1)) {          // a last tile: columns that the row does not attend become -inf
-          uint64_t keep = kept(ts);
+          uint64_t keep = kept(ts) >> c0;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c, keep >>= 16) {
+          for (int c = 0; c < nch; ++c, keep >>= 16) {
             uint32_t s[16];
-            tmem_ld16(col + 16 * c, s);
+            tmem_ld16(sc0 + 16 * c, s);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = (keep >> e) & 1 ? s[e] : 0xFF800000u;
-            tmem_st16(col + 16 * c, s);
+            tmem_st16(sc0 + 16 * c, s);
           }
           tmem_st_wait();
         }
-        uint32_t s[64];
-        tmem_ld32(col, reinterpret_cast<uint32_t(&)[32]>(s[0]));
-        tmem_ld32(col + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
-        tmem_ld_wait();
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mt = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < nch; ++c) {
+          uint32_t s[16];
+          tmem_ld16(sc0 + 16 * c, s);
+          tmem_ld_wait();
+          float x = mt, y = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 64; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
-        float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          for (int e = 0; e < 16; e += 4) {
+            x = max3(x, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            y = max3(y, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+          }
+          mt = fmaxf(x, y);
+        }
         mt = mt == -INFINITY ? mt : mt * sc;
         const bool first = m == -INFINITY;
         const bool grow = mt > m + kGrow;
@@ -695,20 +705,41 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
         const float base = kPShift - (m == -INFINITY ? 0.f : m);
         const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base);
+        // P of column t lies in half t & 1 of column t / 2: the loop writes behind what it has read
         float2 sum = make_float2(0.f, 0.f);
+        if (fold > 1) {
+          // (first take the columns out of the way of the zeros, which the other copies' columns get)
+          uint32_t s[32];
+          tmem_ld16(sc0, reinterpret_cast<uint32_t(&)[16]>(s[0]));
+          if (nch > 1) tmem_ld16(sc0 + 16, reinterpret_cast<uint32_t(&)[16]>(s[16]));
+          tmem_ld_wait();
+          uint32_t z[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t p[16];
+          for (int e = 0; e < 8; ++e) z[e] = 0u;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c)
+            if (c * 16 < c0 || c * 16 >= c0 + 16 * nch) tmem_st8(col + 8 * c, z);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int c = 32 * k + 2 * e;
-            float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, base2);
-            x.x = ex2(x.x);
-            x.y = ex2(x.y);
-            sum = add2(sum, x);
-            p[e] = h2_bits(x.x, x.y);
+          for (int c = 0; c < 2; ++c) {
+            if (c < nch) {
+              uint32_t p[8];
+              weights(s + 16 * c, sc2, base2, sum, p);
+              tmem_st8(col + (uint32_t)(c0 / 2) + 8 * c, p);
+            }
           }
-          tmem_st16(col + 16 * k, p);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t s[32];
+            tmem_ld32(col + 32 * c, s);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t p[8];
+              weights(s + 16 * h, sc2, base2, sum, p);
+              tmem_st8(col + 16 * c + 8 * h, p);
+            }
+          }
         }
         l += sum.x + sum.y;
         tmem_st_wait();
@@ -807,22 +838,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll 1
     for (int i = 0; ok && i < n + kAhead; ++i) {
       if (i < n) {
-        const int st = i % kStages, ph = i / kStages;
         // S takes the columns of P of four tiles before: its products are in
-        if (!wait_all(&bar->kfull[st], ph)) { fail(609); ok = false; break; }
-        if (!wait_all(&bar->vempty[st], ph + 1)) { fail(610); ok = false; break; }
+        const int st = i % kStages, ph = i / kStages;
+        if (!bar_wait2(&bar->kfull[st], ph, &bar->vempty[st], ph + 1, abort_v, A.wait)) { fail(609); ok = false; break; }
         tc_fence_after();
         const uint32_t kb = k0 + st * kKBytes, d = tmem + (uint32_t)(kColS + 64 * st);
 #pragma unroll 4
         for (int k = 0; k < 16; ++k)
           mma_ts_warp(d, tmem + (uint32_t)(kColQ + 8 * k), desc_sw128(kb + (k >> 2) * (kTileTok * 128) + (k & 3) * 32), id_s, k ? 1u : 0u);
         mma_commit_warp(&bar->sfull[st]);
-        mma_commit_warp(&bar->kempty[st]);
         if (i == n - 1) mma_commit_warp(&bar->klast);
       }
       if (i >= kAhead) {
         const int p = i - kAhead, st = p % kStages, ph = p / kStages;
-        if (!wait_all(&bar->vfull[st], ph) || !wait_all(&bar->pfull[st], ph)) { fail(611); ok = false; break; }
+        if (!bar_wait2(&bar->vfull[st], ph, &bar->pfull[st], ph, abort_v, A.wait)) { fail(611); ok = false; break; }
         tc_fence_after();
         const uint32_t vb = v0 + st * kVBytes, a = tmem + (uint32_t)(kColS + 64 * st);
 #pragma unroll
@@ -1001,7 +1030,7 @@ int launch_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, 
   A.fold = A.R <= kRows / 4 ? 4 : A.R <= kRows / 2 ? 2 : 1;
   A.nsplit = W.nsplit; A.chunk = W.chunk;
   A.words = (T + 63) / 64;
-  A.max_len = max_len;
+  A.max_len = (int)max_len;
   A.scale_log2 = fabsf(scale) * 1.4426950408889634f;
   A.sign = scale < 0.f ? -1.f : 1.f;
   A.q = q; A.out = out;
@@ -1035,7 +1064,8 @@ int launch_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, 
   if (table) {
     A.page = page;
     A.max_pages = (int)(max_len / page);
-    A.npages = pool / ((int64_t)Hkv * page);
+    A.page_inv = (uint32_t)((1ull << 32) / (uint64_t)page);
+    A.npages = (int)(pool / ((int64_t)Hkv * page));
   }
   const int key_bits = kctx[0]->lay.planes;
   if (q_dtype == TQ_DTYPE_F32) return launch_typed<float>(A, G, key_bits, st);
