@@ -289,7 +289,9 @@ template <int P>
 __device__ __forceinline__ void decode_keys(const uint32_t (&x)[8], const TreeGroup& t, float n, float rn, uint8_t* lev,
                                             uint8_t* sgn, int row) {
   const uint32_t nn = h2_bits(n, n);
-  const uint32_t rr = h2_bits(n * rn, n * rn) | 0x80008000u;    // (a set sign bit turns it positive)
+  // the bytes of +-||k|| ||r||; a set sign bit turns it positive
+  const uint32_t rr = h2_bits(n * rn, n * rn);
+  const uint32_t rl = prmt(rr, 0u, 0x0000u), rh = prmt(rr, 0u, 0x1111u) | 0x80808080u;
   const int sw = row & 7;
   uint32_t y[P];
 #pragma unroll
@@ -306,9 +308,9 @@ __device__ __forceinline__ void decode_keys(const uint32_t (&x)[8], const TreeGr
         const uint32_t lb = prmt(t.klo[0], t.klo[1], sl), hb = prmt(t.khi[0], t.khi[1], sl);
         o[2 * h] = mul_h2(prmt(lb, hb, 0x5140u), nn);
         o[2 * h + 1] = mul_h2(prmt(lb, hb, 0x7362u), nn);
-        const uint32_t tb = top_bits<P>(y, u, h);
-        s[2 * h] = (prmt(tb, 0u, 0x1404u) & 0x80008000u) ^ rr;
-        s[2 * h + 1] = (prmt(tb, 0u, 0x3424u) & 0x80008000u) ^ rr;
+        const uint32_t sb = (top_bits<P>(y, u, h) & 0x80808080u) ^ rh;
+        s[2 * h] = prmt(rl, sb, 0x5140u);
+        s[2 * h + 1] = prmt(rl, sb, 0x7362u);
       }
       const int c = ((4 * g + u) ^ sw) << 4;
       *reinterpret_cast<uint4*>(lev + c) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       if (sh && w + 1 < A.words) bits |= __ldg(mr + w + 1) << (64 - sh);
       return keep & bits;
     };
-    const int copy = (32 * warp) / per, nch = 4 / fold, c0 = copy * 16 * nch;      // (a warp's lanes are of one copy)
+    const int copy = (32 * warp) / per, c0 = copy * (64 / fold);      // (a warp's lanes are of one copy)
     // sixteen columns of S to eight of P
     auto weights = [&](const uint32_t* s, float2 sc2, float2 base2, float2& sum, uint32_t (&p)[8]) {
 #pragma unroll
@@ -649,36 +651,43 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       if (!wait_all(&bar->sfull[st], ph)) { fail(604); ok = false; break; }
       tc_fence_after();
       if (warp_live) {
-        // this copy's columns, 16 at a time: c0 .. c0 + 16 nch
-        const uint32_t col = lane_base + (uint32_t)(kColS + 64 * st), sc0 = col + (uint32_t)c0;
+        // this copy's columns: from c0 on, 64 / fold of them
+        const uint32_t col = lane_base + (uint32_t)(kColS + 64 * st);
+        uint32_t s[64];
+        if (fold == 1) {
+          tmem_ld32(col, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+          tmem_ld32(col + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
+        } else {
+          tmem_ld16(col + (uint32_t)c0, reinterpret_cast<uint32_t(&)[16]>(s[0]));
+          if (fold == 2) tmem_ld16(col + (uint32_t)c0 + 16, reinterpret_cast<uint32_t(&)[16]>(s[16]));
+        }
+        tmem_ld_wait();
         const int ts = t0 + i * kTileTok;
         if (ts + kTileTok > min(ctx, t1)) {          // a last tile: columns that the row does not attend become -inf
-          uint64_t keep = kept(ts) >> c0;
-#pragma unroll 1
-          for (int c = 0; c < nch; ++c, keep >>= 16) {
-            uint32_t s[16];
-            tmem_ld16(sc0 + 16 * c, s);
-            tmem_ld_wait();
+          const uint64_t keep = kept(ts) >> c0;
+          auto cut = [&](uint32_t* x, uint32_t bits) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] = (keep >> e) & 1 ? s[e] : 0xFF800000u;
-            tmem_st16(sc0 + 16 * c, s);
+            for (int e = 0; e < 16; ++e) x[e] = (bits >> e) & 1 ? x[e] : 0xFF800000u;
+          };
+          cut(s, (uint32_t)keep);
+          if (fold < 4) cut(s + 16, (uint32_t)(keep >> 16));
+          if (fold < 2) {
+            cut(s + 32, (uint32_t)(keep >> 32));
+            cut(s + 48, (uint32_t)(keep >> 48));
           }
-          tmem_st_wait();
         }
-        float mt = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-          uint32_t s[16];
-          tmem_ld16(sc0 + 16 * c, s);
-          tmem_ld_wait();
-          float x = mt, y = -INFINITY;
+        auto most = [&](const uint32_t* x) {
+          float a = -INFINITY, z = -INFINITY;
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            x = max3(x, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-            y = max3(y, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+            a = max3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            z = max3(z, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
           }
-          mt = fmaxf(x, y);
-        }
+          return fmaxf(a, z);
+        };
+        float mt = most(s);
+        if (fold < 4) mt = fmaxf(mt, most(s + 16));
+        if (fold < 2) mt = max3(mt, most(s + 32), most(s + 48));
         mt = mt == -INFINITY ? mt : mt * sc;
         const bool first = m == -INFINITY;
         const bool grow = mt > m + kGrow;
@@ -705,41 +714,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
         const float base = kPShift - (m == -INFINITY ? 0.f : m);
         const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base);
-        // P of column t lies in half t & 1 of column t / 2: the loop writes behind what it has read
+        // P of column t lies in half t & 1 of column t / 2; the other copies' columns get zeros
         float2 sum = make_float2(0.f, 0.f);
-        if (fold > 1) {
-          // (first take the columns out of the way of the zeros, which the other copies' columns get)
-          uint32_t s[32];
-          tmem_ld16(sc0, reinterpret_cast<uint32_t(&)[16]>(s[0]));
-          if (nch > 1) tmem_ld16(sc0 + 16, reinterpret_cast<uint32_t(&)[16]>(s[16]));
-          tmem_ld_wait();
-          uint32_t z[8];
+        uint32_t p[16];
+        if (fold == 4) {
+          uint32_t z[8], w8[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) z[e] = 0u;
-#pragma unroll 1
+          weights(s, sc2, base2, sum, w8);
+#pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (c * 16 < c0 || c * 16 >= c0 + 16 * nch) tmem_st8(col + 8 * c, z);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (c < nch) {
-              uint32_t p[8];
-              weights(s + 16 * c, sc2, base2, sum, p);
-              tmem_st8(col + (uint32_t)(c0 / 2) + 8 * c, p);
-            }
-          }
+            if (c != copy) tmem_st8(col + 8 * c, z);
+          tmem_st8(col + 8 * copy, w8);
         } else {
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t s[32];
-            tmem_ld32(col + 32 * c, s);
-            tmem_ld_wait();
+          weights(s, sc2, base2, sum, reinterpret_cast<uint32_t(&)[8]>(p[0]));
+          weights(s + 16, sc2, base2, sum, reinterpret_cast<uint32_t(&)[8]>(p[8]));
+          tmem_st16(col + (uint32_t)(c0 / 2), p);
+          if (fold == 2) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t p[8];
-              weights(s + 16 * h, sc2, base2, sum, p);
-              tmem_st8(col + 16 * c + 8 * h, p);
-            }
+            for (int e = 0; e < 16; ++e) p[e] = 0u;
+          } else {
+            weights(s + 32, sc2, base2, sum, reinterpret_cast<uint32_t(&)[8]>(p[0]));
+            weights(s + 48, sc2, base2, sum, reinterpret_cast<uint32_t(&)[8]>(p[8]));
           }
+          tmem_st16(col + (uint32_t)(16 - c0 / 2), p);
         }
         l += sum.x + sum.y;
         tmem_st_wait();
