@@ -468,15 +468,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   const int split = blockIdx.x % A.nsplit;
   const int rt = (blockIdx.x / A.nsplit) % A.tiles_r;
   const int bh = blockIdx.x / (A.nsplit * A.tiles_r), b = bh / A.Hkv, hk = bh % A.Hkv;
+  const int r0 = rt * kRows;
+  const int nrow = min(kRows, A.R - r0);                 // rows of this tile
+  // the matrices and rows of the projection are on their way while the lengths come
+  copy_matrix<TWO ? 64 : 128>(smem + kOffPi, A.g[0].pi, threadIdx.x, kThreads);
+  copy_matrix<TWO ? 64 : 128>(smem + kOffS, A.g[0].st, threadIdx.x, kThreads);
+  if (TWO) {
+    copy_matrix<64>(smem + kOffPi + 8192, A.g[1].pi, threadIdx.x, kThreads);
+    copy_matrix<64>(smem + kOffS + 8192, A.g[1].st, threadIdx.x, kThreads);
+  }
+  constexpr int kChunks = kTD * (int)sizeof(T) / 16;
+#pragma unroll 1
+  for (int e = threadIdx.x; e < nrow * kChunks; e += kThreads) {
+    const int r = e / kChunks, c = e % kChunks;
+    copy16(smem + kOffV + e * 16, static_cast<const uint8_t*>(A.q) + q_row(A, b, hk, r0 + r) * kTD * sizeof(T) + c * 16);
+  }
   int len, nd;
   lens_of(A, b, len, nd);
   const int ctx = len - nd;
-  const int r0 = rt * kRows;
-  const int nrow = min(kRows, A.R - r0);                 // rows of this tile
   const int live = min(nrow, nd * A.rep - r0);           // those of drafted tokens that exist
   const int t0 = split * A.chunk, t1 = min(len, t0 + A.chunk);
   const int32_t* perm = A.perm ? A.perm + (size_t)hk * kTD : nullptr;
   if (live <= 0 || t0 >= t1) {                           // nothing to attend: zeros (the merge writes its own)
+    copy_wait();
     if (A.nsplit == 1)
 #pragma unroll 1
       for (int r = warp; r < nrow; r += kThreads / 32)
@@ -517,8 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   auto wait_all = [&](uint64_t* x, int parity) { return __all_sync(0xffffffffu, bar_wait(x, parity, abort_v, A.wait)) != 0; };
   uint32_t tmem = 0;
   // ------------------------------------------------------------------ projection of the rows
-  // Rows and matrices come in as asynchronous copies; then a warp a row makes fp16 operands of them,
-  // scaled by a power of two so that the largest element is near 2^9, every copy of them.
+  // A warp a row makes fp16 operands of the rows, scaled by a power of two so that the largest element is near 2^9, every copy of them.
   const int dw = warp - kSoftWarps, half = (dw % kDecSet) >> 1, set = dw / kDecSet, drow = 32 * (dw & 1) + lane;
   Decoder dec;
   if (warp >= kSoftWarps && warp < kMmaWarp) {
@@ -528,18 +541,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   }
   bool ok = true;
   {
-    copy_matrix<TWO ? 64 : 128>(smem + kOffPi, A.g[0].pi, threadIdx.x, kThreads);
-    copy_matrix<TWO ? 64 : 128>(smem + kOffS, A.g[0].st, threadIdx.x, kThreads);
-    if (TWO) {
-      copy_matrix<64>(smem + kOffPi + 8192, A.g[1].pi, threadIdx.x, kThreads);
-      copy_matrix<64>(smem + kOffS + 8192, A.g[1].st, threadIdx.x, kThreads);
-    }
-    constexpr int kChunks = kTD * (int)sizeof(T) / 16;
-#pragma unroll 1
-    for (int e = threadIdx.x; e < live * kChunks; e += kThreads) {
-      const int r = e / kChunks, c = e % kChunks;
-      copy16(smem + kOffV + e * 16, static_cast<const uint8_t*>(A.q) + q_row(A, b, hk, r0 + r) * kTD * sizeof(T) + c * 16);
-    }
     copy_wait();
     __syncthreads();
     int4 ch = make_int4(4 * lane, 4 * lane + 1, 4 * lane + 2, 4 * lane + 3);
@@ -948,9 +949,11 @@ struct TreeWs {
   int nsplit, chunk;
 };
 
-// Splits of the tokens: as many as give the shortest modelled time, waves of CTAs (one per SM)
-// times (tiles per CTA + the cost of a CTA's start and end, about kEdge tiles).
-constexpr int kEdge = 8, kMaxSplit = 128;
+// Splits of the tokens: as many as give the shortest modelled time, in tiles: a CTA takes its tiles
+// and kEdge more for its start and end (20,000 cycles, a tile about 1,400); more CTAs than SMs take
+// between their share (lengths differ, and a free SM takes the next CTA) and whole waves; splits
+// cost a merge launch.
+constexpr int kEdge = 14, kMergeTiles = 4, kMaxSplit = 128;
 
 TreeWs tree_ws(int B, int T, int Hq, int Hkv, int64_t max_len) {
   TreeWs w{};
@@ -967,7 +970,9 @@ TreeWs tree_ws(int B, int T, int Hq, int Hkv, int64_t max_len) {
   for (int64_t s = 1; s <= std::min<int64_t>(kMaxSplit, tiles); ++s) {
     const int64_t per = (tiles + s - 1) / s;
     if (s > 1 && (tiles + per - 1) / per < s) continue;        // same split as a smaller s
-    const double t = (double)((std::max<int64_t>(1, ctas) * s + sms - 1) / sms) * (double)(per + kEdge);
+    const int64_t all = std::max<int64_t>(1, ctas) * s;
+    const double waves = all <= sms ? 1.0 : 0.5 * ((double)((all + sms - 1) / sms) + (double)all / sms);
+    const double t = waves * (double)(per + kEdge) + (s > 1 ? kMergeTiles : 0);
     if (t < best_t - 1e-9) {
       best_t = t;
       best = s;
