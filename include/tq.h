@@ -411,7 +411,7 @@ int tq_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head, co
  * NaN score comes last.  A sequence with at most `select` pages attends all of them.
  * selected (device int32 [B][Hkv][select], may be NULL): the attended pages (logical numbers) in
  * ascending order, -1 behind the last.  out: device [B][Hq][D] of q_dtype (F32, BF16 or F16).
- * bounds: as kept by tq_page_bounds (bounds_dtype, bounds_pages pages).  block_table, page_tokens and
+ * bounds: as kept by tq_page_bounds (bounds_dtype, bounds_pages pages), 16-byte aligned.  block_table, page_tokens and
  * channel_perm as in tq_decode_opts; the table is required, the permutation may be NULL.  Other
  * arguments, supported caches and errors as tq_decode_attention_ex; TQ_ERR_INVALID_ARG too for select < 1,
  * negative first or last, a NULL table or bounds.  An entry of the table outside the caches reads page

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -104,7 +105,7 @@ def lib():
         "tq_quantize_kv_cols": (I, [P, P, I, I64, I64, P, PK, P, P, SZ, P]),
         "tq_search_workspace_size": (SZ, [P, I64, I64, I]),
         "tq_search_topk": (I, [P, P, I64, PK, I64, I, P, P, P, SZ, P]),
-        "tq_rope": (I, [ctypes.POINTER(_RopeTensor), I, I, I64, I, I, P, P, I, ctypes.c_double, I, P]),
+        "tq_rope": (I, [P, I, I, I64, I, I, P, P, I, ctypes.c_double, I, P]),
         "tq_rope_frequencies": (I, [I, ctypes.c_double, ctypes.POINTER(_RopeScaling), P, ctypes.POINTER(ctypes.c_double)]),
         "tq_page_bounds": (I, [P, I, I64, I64, P, P, I, I, I, I64, P, I, I, P, I64, P]),
         "tq_sparse_workspace_size": (SZ, [I, I, I, I, I, I64, I, I]),
@@ -154,12 +155,17 @@ def _ptr(t) -> ctypes.c_void_p:
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
 
 
+_CODES = {}
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
-    if t.dtype not in codes:
+    if not _CODES:
+        torch = _torch()
+        _CODES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
+    code = _CODES.get(t.dtype)
+    if code is None:
         raise TypeError("unsupported dtype %s" % t.dtype)
-    return codes[t.dtype]
+    return code
 
 
 def _rows(t, d: int):
@@ -402,17 +408,24 @@ def search_topk(ctx: Context, q, db: Packed, N: int, k: int, stream=None):
 ROPE_SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 
 
+def _raw_stream(stream) -> int:
+    """Address of the stream; the current one of the current device when None (without building a Stream object)."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _on_current_device(*tensors):
     """Every call launches on the current device: a tensor of another one (or of the host) is refused."""
-    dev = _torch().cuda.current_device()
+    dev = _torch()._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:      # (-1 for the host)
             raise ValueError("expected CUDA tensors on the current device (cuda:%d), got one on %s" % (dev, t.device))
 
 
 def _int32(t, shape, name):
-    torch = _torch()
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not _torch().int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, tuple(shape)))
 
 
@@ -436,28 +449,40 @@ def rope(q, k, positions, freqs, *, interleaved: bool = False, factor: float = 1
     positions int32 / int64 CUDA [n]; freqs float64 CUDA [rot/2]; channels from rot on are copied.  The outputs may
     be q and k themselves.  transpose=True turns back: the gradient of the call without it."""
     torch = _torch()
-    D, n = q.shape[-1], q.shape[0]
-    sides = (_RopeTensor * 2)()
-    outs = []
-    given = ((q, q_out),) if k is None else ((q, q_out), (k, k_out))
-    for i, (x, out) in enumerate(given):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if x.dim() != 3 or x.shape[0] != n or x.shape[2] != D or out.shape != x.shape or x.dtype != q.dtype \
-                or out.dtype != q.dtype or x.stride(2) != 1 or out.stride(2) != 1:
-            raise ValueError("q, k and their outputs must be [n, heads, D] of one dtype with unit stride along channels")
-        xs, os_ = x.stride(), out.stride()
-        sides[i] = _RopeTensor(x.data_ptr(), out.data_ptr(), x.shape[1], xs[0], xs[1], os_[0], os_[1])
-        outs.append(out)
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 tensor [rot/2]")
-    if positions.dtype not in (torch.int32, torch.int64) or positions.shape != (n,) or not positions.is_contiguous():
+    n, wide = q.shape[0], positions.dtype is torch.int64
+    if not (wide or positions.dtype is torch.int32) or positions.shape != (n,) or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 or int64 tensor [n]")
-    _on_current_device(q, k, positions, freqs, *outs)
-    _check(lib().tq_rope(sides, len(given), _dtype_code(q), n, D, 2 * freqs.shape[0], freqs.data_ptr(),
-                         positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32, factor,
-                         (1 if interleaved else 0) | (2 if transpose else 0), _stream(stream)))
-    return outs[0], (outs[1] if k is not None else None)
+    q_out, args = _rope_side(q, q_out, q)
+    count = 1
+    if k is not None:
+        k_out, more = _rope_side(k, k_out, q)
+        args += more
+        count = 2
+    _on_current_device(q, k, positions, freqs, q_out, k_out)
+    _check(lib().tq_rope(_ROPE_SIDES[count].pack(*args), count, _dtype_code(q), n, q.shape[2], 2 * freqs.shape[0],
+                         freqs.data_ptr(), positions.data_ptr(), 64 if wide else 32, factor,
+                         (1 if interleaved else 0) | (2 if transpose else 0), _raw_stream(stream)))
+    return q_out, k_out
+
+
+_ROPE_SIDES = {n: struct.Struct("@" + n * "PPi4xqqqq") for n in (1, 2)}     # tq_rope_tensor, n times
+
+
+def _rope_side(x, out, q):
+    """(output, fields of a tq_rope_tensor) of one tensor of the call."""
+    if out is None:
+        out = _torch().empty_like(x)
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != q.shape[0] or shape[2] != q.shape[2] or out.shape != shape \
+            or x.dtype is not q.dtype or out.dtype is not q.dtype:
+        raise ValueError("q, k and their outputs must be [n, heads, D] of one dtype")
+    xt, xh, xc = x.stride()
+    ot, oh, oc = out.stride()
+    if xc != 1 or oc != 1:
+        raise ValueError("q, k and their outputs must have unit stride along channels")
+    return out, (x.data_ptr(), out.data_ptr(), shape[1], xt, xh, ot, oh)
 
 
 def alloc_page_bounds(npages: int, Hkv: int, D: int, dtype, device=None):
@@ -470,7 +495,7 @@ def page_bounds(k, cu_new, start, block_table, page_tokens: int, bounds, max_new
     """Fold the new keys k [rows, Hkv, D] into the bounds of their pages (in place) -> bounds.  Sequence b appends
     rows cu_new[b] .. cu_new[b+1]-1 as its tokens start[b], ...; max_new >= the largest number of new rows."""
     if k.dim() != 3 or k.stride(2) != 1 or bounds.dtype != k.dtype or not bounds.is_contiguous() \
-            or bounds.dim() != 4 or tuple(bounds.shape[1:]) != (k.shape[1], 2, k.shape[2]):
+            or bounds.dim() != 4 or bounds.shape[1:] != (k.shape[1], 2, k.shape[2]):
         raise ValueError("k must be [rows, Hkv, D] with unit stride along channels, bounds contiguous [pages, Hkv, 2, D] of its dtype")
     B = start.shape[0]
     _int32(start, (B,), "start")
@@ -479,7 +504,7 @@ def page_bounds(k, cu_new, start, block_table, page_tokens: int, bounds, max_new
     _on_current_device(k, cu_new, start, block_table, bounds)
     _check(lib().tq_page_bounds(k.data_ptr(), _dtype_code(k), k.stride(0), k.stride(1), cu_new.data_ptr(), start.data_ptr(),
                                 B, k.shape[1], k.shape[2], int(max_new), block_table.data_ptr(), int(page_tokens),
-                                block_table.shape[1], bounds.data_ptr(), bounds.shape[0], _stream(stream)))
+                                block_table.shape[1], bounds.data_ptr(), bounds.shape[0], _raw_stream(stream)))
     return bounds
 
 
@@ -501,12 +526,13 @@ class _CachePlan:
         return _torch().empty(max(need, 1), dtype=_torch().uint8, device=self.device)
 
     def _query(self, q, shape, out):
-        if tuple(q.shape) != shape:
+        if q.shape != shape:
             raise ValueError("q must be %s, got %s" % (shape, tuple(q.shape)))
-        q = q.contiguous()
+        if not q.is_contiguous():
+            q = q.contiguous()
         if out is None:
-            out = _torch().empty(shape, dtype=q.dtype, device=q.device)
-        elif tuple(out.shape) != shape or out.dtype != q.dtype or not out.is_contiguous():
+            out = _torch().empty_like(q)
+        elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, with the shape and dtype of q")
         return q, out
 
@@ -540,7 +566,7 @@ class SparsePlan(_CachePlan):
     def __call__(self, q, bounds, seq_lens, scale: float, out=None, stream=None):
         """q [B, Hq, D] -> (out [B, Hq, D] of q's dtype, selected int32 [B, Hkv, select]: the plan's own tensor)."""
         q, out = self._query(q, (self.B, self.Hq, self.D), out)
-        if bounds.dim() != 4 or tuple(bounds.shape[1:]) != (self.Hkv, 2, self.D) or not bounds.is_contiguous():
+        if bounds.dim() != 4 or bounds.shape[1:] != (self.Hkv, 2, self.D) or not bounds.is_contiguous():
             raise ValueError("bounds must be contiguous [pages, Hkv, 2, D]")
         _int32(seq_lens, (self.B,), "seq_lens")
         _on_current_device(q, bounds, seq_lens, out)
@@ -549,7 +575,7 @@ class SparsePlan(_CachePlan):
         _check(lib().tq_sparse_decode_attention(
             self._k, self._v, self._off, self.G, q.data_ptr(), _dtype_code(q), self._kc, self._vc, seq_lens.data_ptr(),
             self.B, self.Hq, self.Hkv, self.D, self.max_len, scale, out.data_ptr(), ctypes.byref(o),
-            self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
+            self.workspace.data_ptr(), self.workspace.numel(), _raw_stream(stream)))
         return out, self.selected
 
 
@@ -607,14 +633,14 @@ class TreePlan(_CachePlan):
         _int32(seq_lens, (self.B,), "seq_lens")
         if draft_lens is not None:
             _int32(draft_lens, (self.B,), "draft_lens")
-        if mask is not None and (mask.dtype != torch.int64 or not mask.is_contiguous()
-                                 or tuple(mask.shape) != (self.B, self.T, (self.T + 63) // 64)):
+        if mask is not None and (mask.dtype is not torch.int64 or not mask.is_contiguous()
+                                 or mask.shape != (self.B, self.T, (self.T + 63) // 64)):
             raise ValueError("mask must be a contiguous int64 tensor [B, T, ceil(T / 64)]")
         _on_current_device(q, seq_lens, draft_lens, mask, out)
         _check(lib().tq_tree_attention(
             self._k, self._v, self._off, self.G, q.data_ptr(), _dtype_code(q), self._kc, self._vc, seq_lens.data_ptr(),
-            _ptr(draft_lens), _ptr(mask), self.B, self.T, self.Hq, self.Hkv, self.D, self.max_len, scale, out.data_ptr(),
-            ctypes.byref(self._opts), self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)))
+            None if draft_lens is None else draft_lens.data_ptr(), None if mask is None else mask.data_ptr(), self.B, self.T, self.Hq, self.Hkv, self.D, self.max_len, scale, out.data_ptr(),
+            ctypes.byref(self._opts), self.workspace.data_ptr(), self.workspace.numel(), _raw_stream(stream)))
         return out
 
 

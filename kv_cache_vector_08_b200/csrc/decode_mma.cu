@@ -1173,6 +1173,15 @@ bool decode_caches_supported(const tq_ctx* const* kctx, const tq_ctx* const* vct
   return true;
 }
 
+// The projection of the queries into the decode workspace (every group of a supported cache has the
+// same width, 64 or 128).
+int launch_decode_prep(const tq_ctx* const* kctx, const int* off, int G, const int32_t* perm, const void* q,
+                       int q_dtype, int B, int Hq, int Hkv, int D, int64_t max_len, void* ws, const DecodeView& view,
+                       cudaStream_t st) {
+  float* qp = reinterpret_cast<float*>(static_cast<char*>(ws) + decode_ws(B, Hq, Hkv, D, G, max_len).qp);
+  return launch_prep(q, q_dtype, B * Hq, kctx, off, G, qp, D, perm, view.perm_Hq ? view.perm_Hq : Hq, Hq / Hkv, st);
+}
+
 // Returns kNotHandled when the shape is outside this kernel's instantiations.
 int launch_decode_mma(const tq_ctx* const* kctx, const tq_ctx* const* vctx, const int* off, int G,
                       const int32_t* perm, const int32_t* table, int page, const void* q, int q_dtype,
@@ -1198,8 +1207,8 @@ int launch_decode_mma(const tq_ctx* const* kctx, const tq_ctx* const* vctx, cons
   char* base = static_cast<char*>(ws);
   float* qp = reinterpret_cast<float*>(base + W.qp);
   float* part = reinterpret_cast<float*>(base + W.part);
-  {   // every group of an instantiated kernel has the same width (64 or 128)
-    int r = launch_prep(q, q_dtype, B * Hq, kctx, off, G, qp, D, perm, view.perm_Hq ? view.perm_Hq : Hq, Hq / Hkv, st);
+  if (!view.prepared) {
+    int r = launch_decode_prep(kctx, off, G, perm, q, q_dtype, B, Hq, Hkv, D, max_len, ws, view, st);
     if (r != TQ_OK) return r;
   }
   MmaArgs A{};

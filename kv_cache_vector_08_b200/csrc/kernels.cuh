@@ -24,6 +24,7 @@ DecodeWs decode_ws(int B, int Hq, int Hkv, int D, int G, int64_t max_len);
 struct DecodeView {
   int out_dtype = TQ_DTYPE_F32;
   int perm_Hq = 0, perm_Hkv = 0;   // 0: the call's own
+  bool prepared = false;           // launch_decode_prep ran already (kernels in between launch early)
 };
 size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D, int ngroups, int64_t max_len, int qp_ld);
 int launch_dequantize_tc(const tq_ctx* ctx, const tq_packed* src, const int64_t* slots, int64_t n, float* out,
@@ -39,6 +40,9 @@ int launch_decode_mma(const tq_ctx* const* kctx, const tq_ctx* const* vctx, cons
                       const tq_packed* kc, const tq_packed* vc, const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
                       int64_t max_len, float scale, void* out, void* ws, cudaStream_t st,
                       const DecodeView& view = DecodeView());
+int launch_decode_prep(const tq_ctx* const* kctx, const int* off, int G, const int32_t* perm, const void* q,
+                       int q_dtype, int B, int Hq, int Hkv, int D, int64_t max_len, void* ws, const DecodeView& view,
+                       cudaStream_t st);
 bool decode_caches_supported(const tq_ctx* const* kctx, const tq_ctx* const* vctx, int G, const tq_packed* kc,
                              const tq_packed* vc);
 size_t logits_mma_workspace(int64_t nq, int d);

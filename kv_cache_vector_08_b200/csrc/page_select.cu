@@ -17,6 +17,7 @@
 // decode kernels run on B Hkv sequences of one kv head each, unchanged.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -48,9 +49,9 @@ struct alignas(sizeof(T) * V) Vec {
 
 // ------------------------------------------------------------------------------ bounds
 // CTA = one page of one kv head: thread (row group, vector of V channels) folds every
-// `groups`-th row, the groups meet in shared memory.  Bound: HBM, the rows are read once;
-// four rows a thread are in flight.
-constexpr int kBoundThreads = 128;
+// `groups`-th row, the groups meet in shared memory.  Bound: HBM, the rows are read once; eight rows
+// a thread are in flight, and neighbouring CTAs take the heads of one page, whose rows lie together.
+constexpr int kBoundThreads = 128, kBoundRows = 8;
 
 struct BoundArgs {
   const void* k;
@@ -63,60 +64,80 @@ struct BoundArgs {
   int64_t npages;
 };
 
+// a = min or max of a and b, element by element (a NaN gives way); 16-bit types two at a time.
+template <bool MAX, typename T, int V>
+__device__ __forceinline__ void fold(Vec<T, V>& a, const Vec<T, V>& b) {
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2* x = reinterpret_cast<T2*>(a.v);
+    const T2* y = reinterpret_cast<const T2*>(b.v);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) x[j] = MAX ? __hmax2(x[j], y[j]) : __hmin2(x[j], y[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float u = to_f<T>(a.v[j]), w = to_f<T>(b.v[j]);
+      a.v[j] = from_f<T>(MAX ? fmaxf(u, w) : fminf(u, w));
+    }
+  }
+}
+
 template <typename T, int V>
-__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const BoundArgs A) {
-  extern __shared__ float s_red[];   // [groups][2][D]
-  const int b = blockIdx.z, hk = blockIdx.y;
+__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid_constant__ BoundArgs A) {
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  using VT = Vec<T, V>;
+  VT* s_red = reinterpret_cast<VT*>(s_raw);      // [groups][2][lanes]
+  const int b = blockIdx.z, hk = blockIdx.x % A.Hkv, first = blockIdx.x / A.Hkv, step = gridDim.x / A.Hkv;
   const int lanes = A.D / V, groups = max(1, kBoundThreads / lanes);
   const int64_t r0 = A.cu_new[b], nnew = (int64_t)A.cu_new[b + 1] - r0;
   if (nnew <= 0) return;
   const int64_t t0 = A.start[b], t1 = t0 + nnew;
   if (t0 < 0) return;
   const int64_t last = min((t1 - 1) / A.page, (int64_t)A.max_pages - 1);
-  for (int64_t p = t0 / A.page + blockIdx.x; p <= last; p += gridDim.x) {
-    const int phys = A.table[(size_t)b * A.max_pages + p];
-    const bool live = phys >= 0 && phys < A.npages;   // (the same for the whole CTA)
+  const int32_t* table = A.table + (size_t)b * A.max_pages;
+  int64_t p = t0 / A.page + first;
+  int next = p <= last ? table[p] : 0;           // (a page's entry comes while the page before it is folded)
+  for (; p <= last; p += step) {
+    const int phys = next;
+    if (p + step <= last) next = table[p + step];
+    if (phys < 0 || phys >= A.npages) continue;   // (the same for the whole CTA)
     const int64_t a = max(t0, p * A.page), e = min(t1, (p + 1) * A.page);
-    T* dst = static_cast<T*>(A.bounds) + ((size_t)(live ? phys : 0) * A.Hkv + hk) * 2 * A.D;
-    if (live) {
-      const int g = threadIdx.x / lanes;
-      for (int c = threadIdx.x % lanes; c < lanes && g < groups; c += kBoundThreads) {
-        float lo[V], hi[V];
+    const int g = threadIdx.x / lanes;
+    for (int c = threadIdx.x % lanes; c < lanes && g < groups; c += kBoundThreads) {
+      VT lo, hi;
 #pragma unroll
-        for (int j = 0; j < V; ++j) { lo[j] = INFINITY; hi[j] = -INFINITY; }
-        const T* src = static_cast<const T*>(A.k) + (r0 + (a - t0)) * A.kt + hk * A.kh + (int64_t)c * V;
-#pragma unroll 4
-        for (int64_t r = g; r < e - a; r += groups) {
-          const Vec<T, V> x = *reinterpret_cast<const Vec<T, V>*>(src + r * A.kt);
+      for (int j = 0; j < V; ++j) { lo.v[j] = from_f<T>(INFINITY); hi.v[j] = from_f<T>(-INFINITY); }
+      const T* src = static_cast<const T*>(A.k) + (r0 + (a - t0)) * A.kt + hk * A.kh + (int64_t)c * V;
+      const int rows = (int)(e - a);
+      for (int r = g; r < rows; r += kBoundRows * groups) {
+        VT x[kBoundRows];
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float f = to_f<T>(x.v[j]);
-            lo[j] = fminf(lo[j], f);
-            hi[j] = fmaxf(hi[j], f);
-          }
-        }
+        for (int i = 0; i < kBoundRows; ++i)     // (past the end: the last row again)
+          x[i] = *reinterpret_cast<const VT*>(src + (int64_t)min(r + i * groups, rows - 1) * A.kt);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          s_red[(g * 2) * A.D + c * V + j] = lo[j];
-          s_red[(g * 2 + 1) * A.D + c * V + j] = hi[j];
+        for (int i = 0; i < kBoundRows; ++i) {
+          fold<false>(lo, x[i]);
+          fold<true>(hi, x[i]);
         }
       }
+      s_red[(g * 2) * lanes + c] = lo;
+      s_red[(g * 2 + 1) * lanes + c] = hi;
     }
     __syncthreads();
-    if (live)
-      for (int c = threadIdx.x; c < A.D; c += kBoundThreads) {
-        float lo = INFINITY, hi = -INFINITY;
-        for (int g = 0; g < groups; ++g) {
-          lo = fminf(lo, s_red[(g * 2) * A.D + c]);
-          hi = fmaxf(hi, s_red[(g * 2 + 1) * A.D + c]);
-        }
-        if (a > p * A.page) {       // the page held tokens before this call
-          lo = fminf(lo, to_f<T>(dst[c]));
-          hi = fmaxf(hi, to_f<T>(dst[A.D + c]));
-        }
-        dst[c] = from_f<T>(lo);
-        dst[A.D + c] = from_f<T>(hi);
+    VT* dst = reinterpret_cast<VT*>(static_cast<T*>(A.bounds) + ((size_t)phys * A.Hkv + hk) * 2 * A.D);
+    for (int c = threadIdx.x; c < 2 * lanes; c += kBoundThreads) {
+      VT x = s_red[c];
+      const bool top = c >= lanes;
+      for (int k = 1; k < groups; ++k) {
+        if (top) fold<true>(x, s_red[2 * k * lanes + c]);
+        else fold<false>(x, s_red[2 * k * lanes + c]);
       }
+      if (a > p * A.page) {           // the page held tokens before this call
+        if (top) fold<true>(x, dst[c]);
+        else fold<false>(x, dst[c]);
+      }
+      dst[c] = x;
+    }
     __syncthreads();
   }
 }
@@ -124,7 +145,7 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const BoundA
 template <typename T>
 int launch_bounds_t(const BoundArgs& A, int vec, dim3 grid, cudaStream_t st) {
   const int lanes = A.D / vec, groups = std::max(1, kBoundThreads / lanes);
-  const size_t sm = (size_t)groups * 2 * A.D * sizeof(float);
+  const size_t sm = (size_t)groups * 2 * A.D * sizeof(T);
   if (vec > 1) page_bounds_kernel<T, 16 / (int)sizeof(T)><<<grid, kBoundThreads, sm, st>>>(A);
   else page_bounds_kernel<T, 1><<<grid, kBoundThreads, sm, st>>>(A);
   count_launch();
@@ -132,10 +153,12 @@ int launch_bounds_t(const BoundArgs& A, int vec, dim3 grid, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------ scores
-// CTA = (sequence, kv head, kScorePages pages), 8 warps: q+ and q- of the group are summed
-// once into shared memory, then a warp takes a page at a time: lane l holds channels
-// l, l + 32, ... of both bounds.  Bound: HBM, 4 D bytes a page and head at 16 bits.
-constexpr int kScoreThreads = 256, kScorePages = 64;
+// CTA = (sequence, kv head, 32 pages), 8 warps: q+ and q- of the group are summed once into shared
+// memory; a warp takes four pages, whose bounds are all loaded before the first is summed (lanes
+// 0-15 the minima, 16-31 the maxima, 8 channels each; twice for 32-bit bounds).  Bound: HBM, 4 D
+// bytes a page and head at 16 bits, and before that the latency of the page table and the bounds.
+constexpr int kScoreThreads = 256, kScorePages = 32, kScoreWarpPages = 4;
+constexpr int kSelD = 128;                 // head dimension of the caches that the decode kernels read
 
 struct SelectArgs {
   const void* q;             // [B][Hq][D]
@@ -145,6 +168,7 @@ struct SelectArgs {
   int B, Hq, Hkv, D, page, max_pages;
   int64_t max_len, npages, pool;   // pages of the bounds, pages of the caches
   int select, first, last;
+  int staged;                // pages whose keys fit into shared memory
   uint64_t* key;             // [B Hkv][max_pages] order-preserving scores
   int32_t* selected;         // [B][Hkv][select] or NULL
   int32_t* vtable;           // [B Hkv][select] pages of the one-head view
@@ -162,85 +186,152 @@ __device__ __forceinline__ uint64_t order_key(double s) {
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 template <typename TQ, typename TB>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectArgs A) {
-  extern __shared__ double s_q[];   // [2][D]: sums of the heads' positive and negative parts
+__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ SelectArgs A) {
+  __shared__ double s_q[2 * kSelD];   // sums of the heads' negative parts (for the minima), then of the positive ones
   const int hk = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  dep_launch();
   const int n = (live_tokens(A, b) + A.page - 1) / A.page;
-  const int p0 = blockIdx.x * kScorePages, p1 = min(n, p0 + kScorePages);
-  if (p0 >= p1) return;
+  const int p0 = blockIdx.x * kScorePages + warp * kScoreWarpPages;
   const int rep = A.Hq / A.Hkv;
-  for (int c = threadIdx.x; c < A.D; c += kScoreThreads) {
+  constexpr int kV = 16 / (int)sizeof(TB), kL = 8 / kV;       // channels a load, loads a lane
+  using VT = Vec<TB, kV>;
+  // page entries of the warp's pages, then their bounds
+  int phys = -1;
+  if (lane < kScoreWarpPages && p0 + lane < n) phys = A.table[(size_t)b * A.max_pages + p0 + lane];
+  VT box[kScoreWarpPages][kL];
+#pragma unroll
+  for (int i = 0; i < kScoreWarpPages; ++i) {
+    const int pg = __shfl_sync(0xffffffffu, phys, i);
+    const bool in = pg >= 0 && pg < A.npages;
+    const TB* src = static_cast<const TB*>(A.bounds) + ((size_t)(in ? pg : 0) * A.Hkv + hk) * 2 * kSelD + 8 * lane;
+#pragma unroll
+    for (int j = 0; j < kL; ++j)
+      if (in) box[i][j] = *reinterpret_cast<const VT*>(src + j * kV);
+  }
+  if (threadIdx.x < kSelD) {
     double pos = 0.0, neg = 0.0;
-    const TQ* q = static_cast<const TQ*>(A.q) + ((size_t)b * A.Hq + (size_t)hk * rep) * A.D + c;
+    const TQ* q = static_cast<const TQ*>(A.q) + ((size_t)b * A.Hq + (size_t)hk * rep) * kSelD + threadIdx.x;
+#pragma unroll 4
     for (int h = 0; h < rep; ++h) {
-      const float v = to_f<TQ>(q[(size_t)h * A.D]);
+      const float v = to_f<TQ>(q[(size_t)h * kSelD]);
       if (v > 0.f) pos += v;
       else neg += v;                 // (a NaN makes the score NaN)
     }
-    s_q[c] = pos;
-    s_q[A.D + c] = neg;
+    s_q[threadIdx.x] = neg;
+    s_q[kSelD + threadIdx.x] = pos;
   }
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int p = p0 + warp; p < p1; p += kScoreThreads / 32) {
-    uint64_t key = ~0ull;
-    if (p >= A.first && p < n - A.last) {
-      const int phys = A.table[(size_t)b * A.max_pages + p];
-      double s = 0.0;
-      if (phys >= 0 && phys < A.npages) {
-        const TB* box = static_cast<const TB*>(A.bounds) + ((size_t)phys * A.Hkv + hk) * 2 * A.D;
-        for (int c = lane; c < A.D; c += 32) {
-          const double qp = s_q[c], qn = s_q[A.D + c];
-          // a zero part leaves its bound out (0 * infinity is no bound)
-          if (qp != 0.0) s += qp * (double)to_f<TB>(box[A.D + c]);
-          if (qn != 0.0) s += qn * (double)to_f<TB>(box[c]);
-        }
-      } else {
-        s = -INFINITY;
-      }
+  if (p0 < n) {
+    double q[8], s[kScoreWarpPages];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      key = order_key(s);
-      if (key == ~0ull) --key;
+    for (int j = 0; j < 8; ++j) q[j] = s_q[8 * lane + j];
+#pragma unroll
+    for (int i = 0; i < kScoreWarpPages; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, phys, i);
+      s[i] = 0.0;
+      if (pg >= 0 && pg < A.npages) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (q[j] != 0.0) s[i] = fma(q[j], (double)to_f<TB>(box[i][j / kV].v[j % kV]), s[i]);   // (0 * infinity is no bound)
+      } else {
+        s[i] = -INFINITY;
+      }
     }
-    if (lane == 0) A.key[((size_t)b * A.Hkv + hk) * A.max_pages + p] = key;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < kScoreWarpPages; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+#pragma unroll
+    for (int i = 0; i < kScoreWarpPages; ++i) {
+      const int p = p0 + i;
+      if (lane == i && p < n) {
+        uint64_t key = order_key(s[i]);
+        if (key == ~0ull) --key;
+        if (p < A.first || p >= n - A.last) key = ~0ull;
+        A.key[((size_t)b * A.Hkv + hk) * A.max_pages + p] = key;
+      }
+    }
   }
+  dep_wait();     // (the projection of the queries in front of this kernel is done when this one is)
 }
 
 // ------------------------------------------------------------------------------ selection
 // CTA per (sequence, kv head): the select-th largest key by 8-bit digits (a histogram of the
-// keys that share the prefix found so far, most significant digit first), then one ordered
-// pass that keeps the larger keys and the first of the equal ones.
-constexpr int kSelThreads = 256;
+// keys that share the prefix found so far, from the highest bit in which any two keys differ on),
+// then one ordered pass that keeps the larger keys and the first of the equal ones.  Keys sit in
+// shared memory when they fit.
+constexpr int kSelThreads = 512, kSelStaged = 4096;
 
-__global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const SelectArgs A) {
+__global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_constant__ SelectArgs A) {
+  extern __shared__ uint64_t s_key[];
   __shared__ int hist[256];
   __shared__ int s_warp[kSelThreads / 32][2];
+  __shared__ uint64_t s_and[kSelThreads / 32], s_or[kSelThreads / 32];
   __shared__ uint64_t s_prefix;
   __shared__ int s_need, s_done;
   const int vh = blockIdx.x, b = vh / A.Hkv, hk = vh % A.Hkv;
   const int len = live_tokens(A, b), n = (len + A.page - 1) / A.page;
-  const uint64_t* key = A.key + (size_t)vh * A.max_pages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int want = min(A.select, n);
-  // keys above `bar` are taken, and the first `need` keys equal to it
-  uint64_t bar = 0;
-  int need = 0;
-  if (n <= A.select) {
-    need = n;                         // every page: each key is >= 0, taken by `all` below
-  } else {
-    if (tid == 0) { s_prefix = 0; s_need = want; s_done = 0; }
-    __syncthreads();
-    int shift = 56;
-    for (; shift >= 0; shift -= 8) {
+  const int32_t* table = A.table + (size_t)b * A.max_pages;
+  auto view = [&](int i) {           // page i as a page of the one-head view
+    const int phys = table[i];
+    return phys >= 0 && phys < A.pool ? phys * A.Hkv + hk : -1;
+  };
+  dep_wait();                        // the scores
+  if (n <= A.select) {               // every page
+    for (int i = tid; i < A.select; i += kSelThreads) {
+      if (A.selected) A.selected[(size_t)vh * A.select + i] = i < n ? i : -1;
+      A.vtable[(size_t)vh * A.select + i] = i < n ? view(i) : -1;
+    }
+    if (tid == 0) A.vlen[vh] = len;
+    return;
+  }
+  const uint64_t* gkey = A.key + (size_t)vh * A.max_pages;
+  const bool staged = n <= A.staged;
+  uint64_t all_and = ~0ull, all_or = 0;
+  for (int i = tid; i < n; i += kSelThreads) {
+    const uint64_t k = gkey[i];
+    if (staged) s_key[i] = k;
+    if (k != ~0ull) { all_and &= k; all_or |= k; }     // (the pages taken in any case have no score)
+  }
+  const uint64_t* key = staged ? s_key : gkey;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all_and &= __shfl_xor_sync(0xffffffffu, all_and, o);
+    all_or |= __shfl_xor_sync(0xffffffffu, all_or, o);
+  }
+  if (lane == 0) { s_and[warp] = all_and; s_or[warp] = all_or; }
+  __syncthreads();
+  for (int w = 0; w < kSelThreads / 32; ++w) { all_and &= s_and[w]; all_or |= s_or[w]; }
+  // keys above `bar` are taken, and the first `need` keys equal to it; forced pages (all ones) first
+  int forced = 0;
+  {
+    const int last = max(0, n - A.last);
+    forced = min(n, A.first) + n - max(last, min(n, A.first));
+  }
+  const int want = A.select;
+  uint64_t bar = ~0ull, mask = ~0ull;
+  int need = want;                   // (more pages forced than wanted: the first of them)
+  if (forced < want) {
+    const uint64_t diff = all_and ^ all_or;
+    const int high = diff ? 63 - __clzll((long long)diff) : 0;
+    int shift = max(0, high - 7);    // the first digit
+    if (tid == 0) { s_prefix = high + 1 < 64 ? all_and & (~0ull << (high + 1)) : 0; s_need = want - forced; s_done = 0; }
+    int width = high + 1 - shift;    // bits of the digit
+    for (;;) {
       for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
       __syncthreads();
       const uint64_t prefix = s_prefix;
-      const uint64_t above = shift == 56 ? 0 : ~0ull << (shift + 8);
+      const uint64_t above = shift + width < 64 ? ~0ull << (shift + width) : 0;
+      const uint32_t digits = (1u << width) - 1;
       for (int i = tid; i < n; i += kSelThreads) {
         const uint64_t k = key[i];
-        if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+        if (k != ~0ull && (k & above) == prefix) atomicAdd(&hist[(uint32_t)(k >> shift) & digits], 1);
       }
       __syncthreads();
       if (warp == 0) {                // digit of the need-th largest key with this prefix
@@ -266,69 +357,73 @@ __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const SelectArgs
         }
       }
       __syncthreads();
-      if (s_done) break;
+      if (s_done || shift == 0) break;
+      width = min(8, shift);
+      shift -= width;
     }
-    // every key whose digits from `shift` on are above or equal to the prefix is taken, down
-    // to the lowest page; with no digits left, only the first s_need of the equal keys
     bar = s_prefix;
     need = s_need;
-    if (shift < 0) shift = 0;
-    const uint64_t mask = ~0ull << shift;
-    // (below, keys are compared by their digits from `shift` on)
-    int base = 0, eq_base = 0;
-    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const uint64_t k = i < n ? key[i] & mask : 0;
-      const bool gt = i < n && k > bar, eq = i < n && k == bar;
-      const unsigned eqm = __ballot_sync(0xffffffffu, eq);
-      if (lane == 0) s_warp[warp][0] = __popc(eqm);
-      __syncthreads();
-      int eq_rank = eq_base + __popc(eqm & ((1u << lane) - 1)), eq_all = 0;
-      for (int w = 0; w < kSelThreads / 32; ++w) {
-        if (w < warp) eq_rank += s_warp[w][0];
-        eq_all += s_warp[w][0];
-      }
-      const bool take = gt || (eq && eq_rank < need);
-      const unsigned tm = __ballot_sync(0xffffffffu, take);
-      if (lane == 0) s_warp[warp][1] = __popc(tm);
-      __syncthreads();
-      int rank = base + __popc(tm & ((1u << lane) - 1)), all = 0;
-      for (int w = 0; w < kSelThreads / 32; ++w) {
-        if (w < warp) rank += s_warp[w][1];
-        all += s_warp[w][1];
-      }
-      if (take) {
-        const int phys = A.table[(size_t)b * A.max_pages + i];
-        if (A.selected) A.selected[(size_t)vh * A.select + rank] = i;
-        A.vtable[(size_t)vh * A.select + rank] = phys >= 0 && phys < A.pool ? phys * A.Hkv + hk : -1;
-        if (rank == want - 1) A.vlen[vh] = i == n - 1 ? (want - 1) * A.page + (len - i * A.page) : want * A.page;
-      }
-      base += all;
-      eq_base += eq_all;
-      __syncthreads();
-    }
-    return;
+    mask = ~0ull << shift;            // (keys are compared by their digits from `shift` on)
   }
-  for (int i = tid; i < A.select; i += kSelThreads) {
-    int v = -1;
-    if (i < n) {
-      const int phys = A.table[(size_t)b * A.max_pages + i];
-      if (phys >= 0 && phys < A.pool) v = phys * A.Hkv + hk;
+  int base = 0, eq_base = 0;
+  for (int i0 = 0; i0 < n && base < want; i0 += kSelThreads) {
+    const int i = i0 + tid;
+    const uint64_t k = i < n ? key[i] : 0;
+    const bool must = forced < want && k == ~0ull;
+    const bool gt = must || (i < n && (k & mask) > bar), eq = !gt && i < n && (k & mask) == bar;
+    const unsigned eqm = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) s_warp[warp][0] = __popc(eqm);
+    __syncthreads();
+    int eq_rank = eq_base + __popc(eqm & ((1u << lane) - 1)), eq_all = 0;
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w < warp) eq_rank += s_warp[w][0];
+      eq_all += s_warp[w][0];
     }
-    if (A.selected) A.selected[(size_t)vh * A.select + i] = i < n ? i : -1;
-    A.vtable[(size_t)vh * A.select + i] = v;
+    const bool take = gt || (eq && eq_rank < need);
+    const unsigned tm = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) s_warp[warp][1] = __popc(tm);
+    __syncthreads();
+    int rank = base + __popc(tm & ((1u << lane) - 1)), all = 0;
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w < warp) rank += s_warp[w][1];
+      all += s_warp[w][1];
+    }
+    if (take) {
+      if (A.selected) A.selected[(size_t)vh * A.select + rank] = i;
+      A.vtable[(size_t)vh * A.select + rank] = view(i);
+      if (rank == want - 1) A.vlen[vh] = i == n - 1 ? (want - 1) * A.page + (len - i * A.page) : want * A.page;
+    }
+    base += all;
+    eq_base += eq_all;
+    __syncthreads();
   }
-  if (tid == 0) A.vlen[vh] = len;
+}
+
+// Launch that may start while the kernel in front of it still runs (it waits for what it needs).
+template <typename K>
+int launch_early(K kern, dim3 grid, int threads, size_t smem, const SelectArgs& A, cudaStream_t st, const char* what) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, A);
+  count_launch();
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return check_launch(what);
 }
 
 template <typename TQ>
 int launch_score_q(const SelectArgs& A, int bounds_dtype, dim3 grid, cudaStream_t st) {
-  const size_t sm = (size_t)2 * A.D * sizeof(double);
-  if (bounds_dtype == TQ_DTYPE_F32) page_score_kernel<TQ, float><<<grid, kScoreThreads, sm, st>>>(A);
-  else if (bounds_dtype == TQ_DTYPE_BF16) page_score_kernel<TQ, __nv_bfloat16><<<grid, kScoreThreads, sm, st>>>(A);
-  else page_score_kernel<TQ, __half><<<grid, kScoreThreads, sm, st>>>(A);
-  count_launch();
-  return check_launch("page_score_kernel");
+  if (bounds_dtype == TQ_DTYPE_F32) return launch_early(page_score_kernel<TQ, float>, grid, kScoreThreads, 0, A, st, "page_score_kernel");
+  if (bounds_dtype == TQ_DTYPE_BF16)
+    return launch_early(page_score_kernel<TQ, __nv_bfloat16>, grid, kScoreThreads, 0, A, st, "page_score_kernel");
+  return launch_early(page_score_kernel<TQ, __half>, grid, kScoreThreads, 0, A, st, "page_score_kernel");
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -343,9 +438,11 @@ int launch_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head
   A.k = k; A.kt = k_token; A.kh = k_head; A.bounds = bounds; A.cu_new = cu_new; A.start = start; A.table = table;
   A.Hkv = Hkv; A.D = D; A.page = page; A.max_pages = max_pages; A.npages = npages;
   const int vec = 16 / es;
-  const bool wide = D % vec == 0 && reinterpret_cast<uintptr_t>(k) % 16 == 0 && k_token % vec == 0 && k_head % vec == 0;
+  const bool wide = D % vec == 0 && reinterpret_cast<uintptr_t>(k) % 16 == 0 && reinterpret_cast<uintptr_t>(bounds) % 16 == 0 && k_token % vec == 0 && k_head % vec == 0;
   const int64_t touched = std::min<int64_t>(max_pages, (max_new + page - 2) / page + 1);
-  const dim3 grid((unsigned)std::min<int64_t>(touched, 65535), (unsigned)Hkv, (unsigned)B);
+  // about 12 CTAs an SM in all, each with pages enough that its first loads (lengths, table) do not count
+  const int64_t ctas = std::max<int64_t>(1, 12 * 148 / ((int64_t)Hkv * B));
+  const dim3 grid((unsigned)(std::min<int64_t>(touched, ctas) * Hkv), 1, (unsigned)B);
   const int v = wide ? vec : 1;
   if (dtype == TQ_DTYPE_F32) return launch_bounds_t<float>(A, v, grid, st);
   if (dtype == TQ_DTYPE_BF16) return launch_bounds_t<__nv_bfloat16>(A, v, grid, st);
@@ -383,9 +480,9 @@ int launch_page_select(const void* q, int q_dtype, const int32_t* seq_lens, int 
     else r = launch_score_q<__half>(A, o->bounds_dtype, grid, st);
     if (r != TQ_OK) return r;
   }
-  page_pick_kernel<<<(unsigned)(B * Hkv), kSelThreads, 0, st>>>(A);
-  count_launch();
-  return check_launch("page_pick_kernel");
+  A.staged = kSelStaged;
+  const size_t sm = A.max_pages > A.select ? (size_t)std::min(A.max_pages, kSelStaged) * sizeof(uint64_t) : 0;
+  return launch_early(page_pick_kernel, dim3((unsigned)(B * Hkv)), kSelThreads, sm, A, st, "page_pick_kernel");
 }
 
 }  // namespace tq

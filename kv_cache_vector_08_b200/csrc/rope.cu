@@ -78,10 +78,73 @@ struct alignas(sizeof(T) * V) Vec {
 };
 
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs A) {
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const __grid_constant__ RopeArgs A) {
   extern __shared__ float2 s_cs[];   // [tb][rot / 2] (cos, sin), times the factor
+  using VT = Vec<T, V>;
+  constexpr bool kTwo = !(INTER && V > 1);    // a unit that rotates has a vector of each half
   const int64_t t0 = (int64_t)blockIdx.x * A.tb;
   const int ntok = (int)(A.n - t0 < A.tb ? A.n - t0 : A.tb), np = A.rot / 2;
+  const int u0 = blockIdx.y * A.chunk, u1 = min(u0 + A.chunk, ntok * A.per_tok.d);
+  // One unit: where it lies, what it holds.
+  struct Unit {
+    T* o;
+    int t, k;                      // token of the block, unit of the head
+    VT a, b;
+  };
+  auto fetch = [&](int u, Unit& x) {
+    x.t = A.per_tok.quot(u);
+    const int r = u - x.t * A.per_tok.d;
+    int h = A.per_head.quot(r);
+    x.k = r - h * A.per_head.d;
+    const bool second = h >= A.heads0;
+    h -= second ? A.heads0 : 0;
+    // (selected field by field: an indexed parameter struct would be copied to local memory)
+    const T* p = static_cast<const T*>(second ? A.s[1].x : A.s[0].x) +
+                 (t0 + x.t) * (second ? A.s[1].xt : A.s[0].xt) + h * (second ? A.s[1].xh : A.s[0].xh);
+    x.o = static_cast<T*>(second ? A.s[1].out : A.s[0].out) +
+          (t0 + x.t) * (second ? A.s[1].ot : A.s[0].ot) + h * (second ? A.s[1].oh : A.s[0].oh);
+    if (x.k >= A.rot_units) {
+      x.a = *reinterpret_cast<const VT*>(p + A.rot + (x.k - A.rot_units) * V);
+    } else if constexpr (kTwo) {
+      // V pairs: vectors of both halves, or (interleaved without alignment) one pair
+      x.a = *reinterpret_cast<const VT*>(p + (INTER ? 2 * x.k : x.k * V));
+      x.b = *reinterpret_cast<const VT*>(p + (INTER ? 2 * x.k + 1 : x.k * V + np));
+    } else {
+      x.a = *reinterpret_cast<const VT*>(p + x.k * V);
+    }
+  };
+  auto turn = [&](Unit& x) {
+    if (x.k >= A.rot_units) {
+      *reinterpret_cast<VT*>(x.o + A.rot + (x.k - A.rot_units) * V) = x.a;
+      return;
+    }
+    const float2* cs = s_cs + x.t * np;
+    if constexpr (kTwo) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float2 w = cs[x.k * V + j];
+        const float x1 = to_f<T>(x.a.v[j]), x2 = to_f<T>(x.b.v[j]);
+        x.a.v[j] = from_f<T>(x1 * w.x - x2 * w.y);
+        x.b.v[j] = from_f<T>(x2 * w.x + x1 * w.y);
+      }
+      *reinterpret_cast<VT*>(x.o + (INTER ? 2 * x.k : x.k * V)) = x.a;
+      *reinterpret_cast<VT*>(x.o + (INTER ? 2 * x.k + 1 : x.k * V + np)) = x.b;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 w = cs[x.k * (V / 2) + j];
+        const float x1 = to_f<T>(x.a.v[2 * j]), x2 = to_f<T>(x.a.v[2 * j + 1]);
+        x.a.v[2 * j] = from_f<T>(x1 * w.x - x2 * w.y);
+        x.a.v[2 * j + 1] = from_f<T>(x2 * w.x + x1 * w.y);
+      }
+      *reinterpret_cast<VT*>(x.o + x.k * V) = x.a;
+    }
+  };
+  // The thread's first unit is on its way while the angles are formed.  (One unit at a time and many
+  // warps: four units a thread need 126 registers, and with 16 warps an SM the 32K prompt took 218 us.)
+  Unit x;
+  int u = u0 + threadIdx.x;
+  if (u < u1) fetch(u, x);
   for (int e = threadIdx.x; e < ntok * np; e += kRopeThreads) {
     const int t = e / np, i = e - t * np;
     const double pos = A.pos64 ? (double)static_cast<const int64_t*>(A.pos)[t0 + t]
@@ -92,50 +155,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs A) {
     s_cs[e] = make_float2(co * A.factor, si * A.factor * A.sign);
   }
   __syncthreads();
-  const int u0 = blockIdx.y * A.chunk, u1 = min(u0 + A.chunk, ntok * A.per_tok.d);
-  using VT = Vec<T, V>;
-#pragma unroll 4
-  for (int u = u0 + threadIdx.x; u < u1; u += kRopeThreads) {
-    const int t = A.per_tok.quot(u), r = u - t * A.per_tok.d;
-    int h = A.per_head.quot(r);
-    const int k = r - h * A.per_head.d;
-    const bool second = h >= A.heads0;
-    h -= second ? A.heads0 : 0;
-    // (selected field by field: an indexed parameter struct would be copied to local memory)
-    const T* x = static_cast<const T*>(second ? A.s[1].x : A.s[0].x) +
-                 (t0 + t) * (second ? A.s[1].xt : A.s[0].xt) + h * (second ? A.s[1].xh : A.s[0].xh);
-    T* o = static_cast<T*>(second ? A.s[1].out : A.s[0].out) +
-           (t0 + t) * (second ? A.s[1].ot : A.s[0].ot) + h * (second ? A.s[1].oh : A.s[0].oh);
-    if (k >= A.rot_units) {
-      const int c = A.rot + (k - A.rot_units) * V;
-      *reinterpret_cast<VT*>(o + c) = *reinterpret_cast<const VT*>(x + c);
-      continue;
-    }
-    const float2* cs = s_cs + t * np;
-    if constexpr (INTER && V > 1) {
-      VT a = *reinterpret_cast<const VT*>(x + k * V);
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float2 w = cs[k * (V / 2) + j];
-        const float x1 = to_f<T>(a.v[2 * j]), x2 = to_f<T>(a.v[2 * j + 1]);
-        a.v[2 * j] = from_f<T>(x1 * w.x - x2 * w.y);
-        a.v[2 * j + 1] = from_f<T>(x2 * w.x + x1 * w.y);
-      }
-      *reinterpret_cast<VT*>(o + k * V) = a;
-    } else {
-      // V pairs: vectors of both halves, or (interleaved without alignment) one pair
-      const int i1 = INTER ? 2 * k : k * V, i2 = INTER ? 2 * k + 1 : k * V + np;
-      VT a = *reinterpret_cast<const VT*>(x + i1), b = *reinterpret_cast<const VT*>(x + i2);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 w = cs[k * V + j];
-        const float x1 = to_f<T>(a.v[j]), x2 = to_f<T>(b.v[j]);
-        a.v[j] = from_f<T>(x1 * w.x - x2 * w.y);
-        b.v[j] = from_f<T>(x2 * w.x + x1 * w.y);
-      }
-      *reinterpret_cast<VT*>(o + i1) = a;
-      *reinterpret_cast<VT*>(o + i2) = b;
-    }
+  while (u < u1) {
+    turn(x);
+    u += kRopeThreads;
+    if (u < u1) fetch(u, x);
   }
 }
 
@@ -149,7 +172,7 @@ int launch_v(RopeArgs A, int heads, bool inter, int sms, cudaStream_t st) {
   // heads), or, when the tokens are too few for the device, slices of one token's heads.
   const int want = 4 * kRopeThreads;
   int64_t tb = std::max<int64_t>(1, want / A.per_tok.d);
-  tb = std::max<int64_t>(1, std::min<int64_t>(tb, A.n / (2 * sms)));
+  tb = std::max<int64_t>(1, std::min<int64_t>(tb, A.n / (4 * sms)));
   tb = std::min<int64_t>(tb, std::max(1, 24 * 1024 / std::max(1, A.rot / 2 * (int)sizeof(float2))));
   A.tb = (int)tb;
   A.per_block = A.tb * A.per_tok.d;

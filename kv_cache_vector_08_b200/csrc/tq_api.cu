@@ -696,8 +696,8 @@ int tq_sparse_decode_attention(const tq_ctx* const* kctx, const tq_ctx* const* v
   if (r != TQ_OK) return r;
   if (B == 0) return TQ_OK;
   if ((r = check_cache_shape((int64_t)B * Hkv * ((Hq / Hkv + 3) / 4), (int64_t)B * Hq, max_len, "tq_sparse_decode_attention")) != TQ_OK) return r;
-  if (!aligned(opts->bounds, elem_size(opts->bounds_dtype)) || !aligned(out, elem_size(q_dtype)) || !aligned(q, elem_size(q_dtype)))
-    return fail(TQ_ERR_UNSUPPORTED, "q, out or bounds not aligned to its element");
+  if (!aligned(opts->bounds, 16) || !aligned(out, elem_size(q_dtype)) || !aligned(q, elem_size(q_dtype)))
+    return fail(TQ_ERR_UNSUPPORTED, "bounds must be 16-byte aligned, q and out to their elements");
   if (!decode_caches_supported(kctx, vctx, ngroups, kcache, vcache)) return unsupported_caches("tq_sparse_decode_attention");
   const SparseWs W = sparse_ws(B, Hq, Hkv, D, ngroups, page, (int)(max_len / page), opts->select);
   if (!workspace || ws_bytes < W.total) return fail(TQ_ERR_WORKSPACE, "workspace too small");
@@ -706,18 +706,25 @@ int tq_sparse_decode_attention(const tq_ctx* const* kctx, const tq_ctx* const* v
   for (int g = 0; g < ngroups; ++g) pool = std::min(pool, std::min(kcache[g].cap, vcache[g].cap));
   pool /= (int64_t)Hkv * page;
   if (pool * Hkv > INT32_MAX) return fail(TQ_ERR_UNSUPPORTED, "more than 2^31 - 1 (page, kv head) pairs");
-  if ((r = launch_page_select(q, q_dtype, seq_lens, B, Hq, Hkv, D, max_len, pool, opts, workspace, W,
-                              (cudaStream_t)stream)) != TQ_OK)
-    return r;
   char* base = static_cast<char*>(workspace);
   DecodeView view;
   view.out_dtype = q_dtype;
   view.perm_Hq = Hq;
   view.perm_Hkv = Hkv;
+  view.prepared = true;
+  const int64_t sel_len = (int64_t)opts->select * page;
+  const DecodeWs dw = decode_ws(B * Hkv, Hq / Hkv, 1, D, ngroups, sel_len);
+  if (dw.nsplit > 512) return fail(TQ_ERR_UNSUPPORTED, "tq_sparse_decode_attention: more than 512 context splits");
+  if ((r = launch_decode_prep(kctx, group_off, ngroups, opts->channel_perm, q, q_dtype, B * Hkv, Hq / Hkv, 1, D, sel_len,
+                              base + W.decode, view, (cudaStream_t)stream)) != TQ_OK)
+    return r;
+  if ((r = launch_page_select(q, q_dtype, seq_lens, B, Hq, Hkv, D, max_len, pool, opts, workspace, W,
+                              (cudaStream_t)stream)) != TQ_OK)
+    return r;
   r = launch_decode_mma(kctx, vctx, group_off, ngroups, opts->channel_perm,
                         reinterpret_cast<const int32_t*>(base + W.vtable), page, q, q_dtype, kcache, vcache,
                         reinterpret_cast<const int32_t*>(base + W.vlen), B * Hkv, Hq / Hkv, 1, D,
-                        (int64_t)opts->select * page, scale, out, base + W.decode, (cudaStream_t)stream, view);
+                        sel_len, scale, out, base + W.decode, (cudaStream_t)stream, view);
   return r == kNotHandled ? fail(TQ_ERR_UNSUPPORTED, "tq_sparse_decode_attention: at most 512 context splits") : r;
 }
 

@@ -918,6 +918,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   int len, nd;
   lens_of(A, b, len, nd);
   const int ns = r / A.rep < nd ? (len + A.chunk - 1) / A.chunk : 0;     // splits that hold tokens
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const float2* ml = A.ml + row * A.nsplit;
   const float4* part = reinterpret_cast<const float4*>(A.part + row * A.nsplit * kTD) + lane;
   float m = -INFINITY;
@@ -1005,8 +1006,19 @@ int launch_typed(const TreeArgs& A, int G, int key_bits, cudaStream_t st) {
   else if (key_bits == 4) r = launch_main<4, 4, 3, 3, true, T>(A, ctas, st);
   else r = launch_main<3, 3, 2, 2, true, T>(A, ctas, st);
   if (r != TQ_OK || A.nsplit == 1) return r;
-  tree_merge_kernel<T><<<(unsigned)(((int64_t)A.B * A.Hkv * A.R + 7) / 8), 256, 0, st>>>(A);
+  // (launches early; it waits for the partials)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((int64_t)A.B * A.Hkv * A.R + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<T>, A);
   count_launch();
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelEx(tree_merge_kernel)");
   return check_launch("tree_merge_kernel");
 }
 
