@@ -51,7 +51,7 @@ struct alignas(sizeof(T) * V) Vec {
 // CTA = one page of one kv head: thread (row group, vector of V channels) folds every
 // `groups`-th row, the groups meet in shared memory.  Bound: HBM, the rows are read once; eight rows
 // a thread are in flight, and neighbouring CTAs take the heads of one page, whose rows lie together.
-constexpr int kBoundThreads = 128, kBoundRows = 8;
+constexpr int kBoundThreads = 128, kBoundRows = 8, kBoundCtas = 8;   // CTAs an SM
 
 struct BoundArgs {
   const void* k;
@@ -83,7 +83,7 @@ __device__ __forceinline__ void fold(Vec<T, V>& a, const Vec<T, V>& b) {
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid_constant__ BoundArgs A) {
+__global__ void __launch_bounds__(kBoundThreads, kBoundCtas) page_bounds_kernel(const __grid_constant__ BoundArgs A) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   using VT = Vec<T, V>;
   VT* s_red = reinterpret_cast<VT*>(s_raw);      // [groups][2][lanes]
@@ -265,10 +265,10 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
 // keys that share the prefix found so far, from the highest bit in which any two keys differ on),
 // then one ordered pass that keeps the larger keys and the first of the equal ones.  Keys sit in
 // shared memory when they fit.
-constexpr int kSelThreads = 512, kSelStaged = 4096;
+constexpr int kSelThreads = 512, kSelStaged = 4096, kSelRank = 384;   // (both ways take as long at about 400 pages)
 
 __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_constant__ SelectArgs A) {
-  extern __shared__ uint64_t s_key[];
+  extern __shared__ __align__(16) uint64_t s_key[];
   __shared__ int hist[256];
   __shared__ int s_warp[kSelThreads / 32][2];
   __shared__ uint64_t s_and[kSelThreads / 32], s_or[kSelThreads / 32];
@@ -292,6 +292,35 @@ __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_con
     return;
   }
   const uint64_t* gkey = A.key + (size_t)vh * A.max_pages;
+  if (n <= kSelRank) {
+    // few pages: every page counts the pages in front of it
+    const int all = (n + 1) & ~1;
+    for (int i = tid; i < all; i += kSelThreads) s_key[i] = i < n ? gkey[i] : 0;
+    __syncthreads();
+    bool take = false;
+    if (tid < n) {
+      const uint64_t k = s_key[tid];
+      int front = 0;
+#pragma unroll 4
+      for (int j = 0; j < all; j += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s_key + j);
+        front += o.x > k || (o.x == k && j < tid);
+        front += o.y > k || (o.y == k && j + 1 < tid);
+      }
+      take = front < A.select;
+    }
+    const unsigned tm = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) s_warp[warp][0] = __popc(tm);
+    __syncthreads();
+    int rank = __popc(tm & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) rank += s_warp[w][0];
+    if (take) {
+      if (A.selected) A.selected[(size_t)vh * A.select + rank] = tid;
+      A.vtable[(size_t)vh * A.select + rank] = view(tid);
+      if (rank == A.select - 1) A.vlen[vh] = tid == n - 1 ? (A.select - 1) * A.page + (len - tid * A.page) : A.select * A.page;
+    }
+    return;
+  }
   const bool staged = n <= A.staged;
   uint64_t all_and = ~0ull, all_or = 0;
   for (int i = tid; i < n; i += kSelThreads) {
@@ -440,8 +469,11 @@ int launch_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head
   const int vec = 16 / es;
   const bool wide = D % vec == 0 && reinterpret_cast<uintptr_t>(k) % 16 == 0 && reinterpret_cast<uintptr_t>(bounds) % 16 == 0 && k_token % vec == 0 && k_head % vec == 0;
   const int64_t touched = std::min<int64_t>(max_pages, (max_new + page - 2) / page + 1);
-  // about 12 CTAs an SM in all, each with pages enough that its first loads (lengths, table) do not count
-  const int64_t ctas = std::max<int64_t>(1, 12 * 148 / ((int64_t)Hkv * B));
+  // one wave of CTAs: each has pages enough that its first loads (lengths, table) do not count, and none
+  // is left for a second, almost empty wave (12 CTAs an SM, of which 9 fit: 77 us for the 128K prompt)
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t ctas = std::max<int64_t>(1, (int64_t)kBoundCtas * sms / ((int64_t)Hkv * B));
   const dim3 grid((unsigned)(std::min<int64_t>(touched, ctas) * Hkv), 1, (unsigned)B);
   const int v = wide ? vec : 1;
   if (dtype == TQ_DTYPE_F32) return launch_bounds_t<float>(A, v, grid, st);
@@ -481,7 +513,7 @@ int launch_page_select(const void* q, int q_dtype, const int32_t* seq_lens, int 
     if (r != TQ_OK) return r;
   }
   A.staged = kSelStaged;
-  const size_t sm = A.max_pages > A.select ? (size_t)std::min(A.max_pages, kSelStaged) * sizeof(uint64_t) : 0;
+  const size_t sm = A.max_pages > A.select ? (size_t)std::min(A.max_pages + 1, kSelStaged) * sizeof(uint64_t) : 0;
   return launch_early(page_pick_kernel, dim3((unsigned)(B * Hkv)), kSelThreads, sm, A, st, "page_pick_kernel");
 }
 
