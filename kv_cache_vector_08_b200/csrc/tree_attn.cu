@@ -282,17 +282,22 @@ __device__ __forceinline__ uint32_t top_bits(const uint32_t (&x)[P], int u, int 
   else return x[P - 1] << (2 * u + h);
 }
 
-// Key rows: levels times the norm, and the residual signs times both norms.  (The loop over the
+// 16 bytes to shared memory at address `at` + `off`.
+template <int off>
+__device__ __forceinline__ void store16(uint32_t at, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0 + %1], {%2, %3, %4, %5};\n" ::"r"(at), "n"(off), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// Key rows: levels times the norm, and the residual signs times both norms.  `at`: shared address of the
+// row's first piece, swizzled (piece c of the row lies at `at` ^ 16 c).  (The loop over the
 // two groups is not unrolled: the warps of a CTA run different code, and short loops keep it in
 // the instruction cache.)
 template <int P>
-__device__ __forceinline__ void decode_keys(const uint32_t (&x)[8], const TreeGroup& t, float n, float rn, uint8_t* lev,
-                                            uint8_t* sgn, int row) {
+__device__ __forceinline__ void decode_keys(const uint32_t (&x)[8], const TreeGroup& t, float n, float rn, uint32_t at) {
   const uint32_t nn = h2_bits(n, n);
   // the bytes of +-||k|| ||r||; a set sign bit turns it positive
   const uint32_t rr = h2_bits(n * rn, n * rn);
   const uint32_t rl = prmt(rr, 0u, 0x0000u), rh = prmt(rr, 0u, 0x1111u) | 0x80808080u;
-  const int sw = row & 7;
   uint32_t y[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) y[i] = x[i];
@@ -312,19 +317,18 @@ __device__ __forceinline__ void decode_keys(const uint32_t (&x)[8], const TreeGr
         s[2 * h] = prmt(rl, sb, 0x5140u);
         s[2 * h + 1] = prmt(rl, sb, 0x7362u);
       }
-      const int c = ((4 * g + u) ^ sw) << 4;
-      *reinterpret_cast<uint4*>(lev + c) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(sgn + c) = make_uint4(s[0], s[1], s[2], s[3]);
+      store16<0>(at ^ (uint32_t)(16 * u), o);
+      store16<2 * kTileTok * 128>(at ^ (uint32_t)(16 * u), s);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) y[i] = x[P + i];
+    at ^= 64u;                      // the second group's pieces
   }
 }
 // Value rows: levels times the norm.
 template <int P>
-__device__ __forceinline__ void decode_values(const uint32_t (&x)[8], const TreeGroup& t, float n, uint8_t* dst, int row) {
+__device__ __forceinline__ void decode_values(const uint32_t (&x)[8], const TreeGroup& t, float n, uint32_t at) {
   const uint32_t nn = h2_bits(n, n);
-  const int sw = row & 7;
   uint32_t y[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) y[i] = x[i];
@@ -342,10 +346,11 @@ __device__ __forceinline__ void decode_values(const uint32_t (&x)[8], const Tree
         o[2 * h] = mul_h2(prmt(lb, hb, 0x5140u), nn);
         o[2 * h + 1] = mul_h2(prmt(lb, hb, 0x7362u), nn);
       }
-      *reinterpret_cast<uint4*>(dst + (((4 * g + u) ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      store16<0>(at ^ (uint32_t)(16 * u), o);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) y[i] = x[P + i];
+    at ^= 64u;                      // the second group's pieces
   }
 }
 
@@ -425,7 +430,8 @@ struct Decode {
   __device__ static __forceinline__ bool loop(Decoder& x, const TreeArgs& A, const TreeGroup& g, uint8_t* smem, Bars* bar,
                                               int half, int set, int row, int b, int hk, int t1, int n,
                                               const volatile int* abort_v, int& code) {
-    const uint32_t part = half * (kTileTok * 128) + row * 128;
+    // the row's first piece of a stage, swizzled
+    const uint32_t at0 = (smem_u32(smem) + half * (kTileTok * 128) + row * 128) ^ ((row & 7) << 4);
     const bool lane0 = (threadIdx.x & 31) == 0;
     auto wait = [&](uint64_t* p, int parity) {
       return __all_sync(0xffffffffu, bar_wait(p, parity, abort_v, A.wait)) != 0;
@@ -437,14 +443,13 @@ struct Decode {
       const bool live = x.live;
       advance(x, A, b, hk, t1);
       if (!wait(&bar->sfull[st], ph + 1)) { code = 601; return false; }
-      uint8_t* lev = smem + st * kKBytes + part;
-      decode_keys<PK>(x.kw, g, live ? f(x.kn) : 0.f, live ? f(x.kr) : 0.f, lev, lev + 2 * (kTileTok * 128), row);
+      decode_keys<PK>(x.kw, g, live ? f(x.kn) : 0.f, live ? f(x.kr) : 0.f, at0 + st * kKBytes);
       load_k(x, g, half);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane0) mbar_arrive(&bar->kfull[st]);
       if (!wait(&bar->vempty[st], ph + 1)) { code = 602; return false; }
-      decode_values<PV>(x.vw, g, live ? f(x.vn) : 0.f, smem + kOffV + st * kVBytes + part, row);
+      decode_values<PV>(x.vw, g, live ? f(x.vn) : 0.f, at0 + kOffV + st * kVBytes);
       load_v(x, g, half);
       fence_proxy_async_smem();
       __syncwarp();
