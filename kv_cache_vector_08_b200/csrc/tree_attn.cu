@@ -40,6 +40,7 @@
 // winds down.
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include "common.cuh"
@@ -91,6 +92,7 @@ struct TreeGroup {
 struct TreeArgs {
   TreeGroup g[2];
   int B, T, Hq, Hkv, rep, R, fold, tiles_r, nsplit, chunk, words;
+  int sort;                       // sequences in the order of their lengths
   int max_len, npages;
   float scale_log2;               // |scale| log2(e)
   float sign;                     // sign of the scale
@@ -470,9 +472,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   // (a shuffle makes the warp's number, and what the products' addresses come from, known to be uniform: the
   // compiler then keeps the operands of the products in uniform registers)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int split = blockIdx.x % A.nsplit;
-  const int rt = (blockIdx.x / A.nsplit) % A.tiles_r;
-  const int bh = blockIdx.x / (A.nsplit * A.tiles_r), b = bh / A.Hkv, hk = bh % A.Hkv;
+  // Blocks go by split, then sequence, then kv head and row tile: the first splits hold the most tokens.
+  // When there are more blocks than SMs, sequences go from the longest to the shortest, so that no long
+  // block starts last: thread t finds the rank of sequence t.
+  const int rt = blockIdx.x % A.tiles_r, hk = blockIdx.x / A.tiles_r % A.Hkv;
+  const int sb = blockIdx.x / (A.tiles_r * A.Hkv), split = sb / A.B;
+  int b = sb % A.B;
+  if (A.sort) {
+    int* s_len = reinterpret_cast<int*>(smem);
+    const int mine = threadIdx.x < A.B ? A.seq_lens[threadIdx.x] : INT_MIN;
+    s_len[threadIdx.x] = mine;
+    __syncthreads();
+    if (threadIdx.x < A.B) {
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < A.B; ++j) rank += s_len[j] > mine || (s_len[j] == mine && j < (int)threadIdx.x);
+      if (rank == b) s_len[kThreads] = threadIdx.x;
+    }
+    __syncthreads();
+    b = s_len[kThreads];
+    __syncthreads();
+  }
+  const int bh = b * A.Hkv + hk;
   const int r0 = rt * kRows;
   const int nrow = min(kRows, A.R - r0);                 // rows of this tile
   // the matrices and rows of the projection are on their way while the lengths come
@@ -953,6 +974,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
 struct TreeWs {
   size_t part, ml, total;
   int nsplit, chunk;
+  bool waves;                     // more blocks than SMs
 };
 
 // Splits of the tokens: as many as give the shortest modelled time, in tiles: a CTA takes its tiles
@@ -987,6 +1009,7 @@ TreeWs tree_ws(int B, int T, int Hq, int Hkv, int64_t max_len) {
   const int64_t per = (tiles + best - 1) / best;
   w.chunk = (int)(per * kTileTok);
   w.nsplit = (int)((tiles + per - 1) / per);
+  w.waves = ctas * w.nsplit > sms;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   w.ml = w.nsplit > 1 ? up((size_t)rows * w.nsplit * kTD * sizeof(float)) : 0;
   w.total = w.nsplit > 1 ? w.ml + up((size_t)rows * w.nsplit * sizeof(float2)) : 256;
@@ -1047,6 +1070,7 @@ int launch_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, 
   TreeArgs A{};
   A.B = B; A.T = T; A.Hq = Hq; A.Hkv = Hkv; A.rep = Hq / Hkv; A.R = T * A.rep;
   A.tiles_r = (A.R + kRows - 1) / kRows;
+  A.sort = W.waves && B > 1 && B <= kThreads;
   A.fold = A.R <= kRows / 4 ? 4 : A.R <= kRows / 2 ? 2 : 1;
   A.nsplit = W.nsplit; A.chunk = W.chunk;
   A.words = (T + 63) / 64;
