@@ -144,7 +144,8 @@ void tq_free(tq_ctx* ctx);
  *            the stall injected by tq_debug_inject_stall)
  *   401-404  workspace quantize path: a pipeline wait exceeded its limit (idem)
  *   501-506  search: a pipeline wait exceeded its limit (idem)
- *   601-614  tree attention: a pipeline wait exceeded its limit (idem)
+ *   601-615  tree attention: a pipeline wait exceeded its limit (idem; 615: the stall
+ *            injected by tq_debug_inject_stall)
  *   901      a device slot array (dst_slot / src_slot) held a slot outside [0, cap): that
  *            row was skipped (quantize) or written as zeros (dequantize)
  *   902      a channel permutation or column map held an entry out of range: that element
@@ -390,16 +391,16 @@ int tq_rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* 
 /* tq_page_bounds -- element-wise bounds of the keys in each page of a paged cache, kept by the caller
  * next to it: bounds (device, of dtype) is [npages][Hkv][2][D] with the minimum, then the maximum, of
  * the keys (rows as given to tq_quantize_kv) of page p and kv head h.  The call folds in new rows:
- * sequence b (B of them) appends rows cu_new[b] .. cu_new[b+1]-1 of k as its tokens start[b], start[b]+1, ...
+ * sequence b (B of them) appends rows cu_new[b] .. cu_new[b+1]-1 of k's n rows as its tokens start[b], start[b]+1, ...
  * (device int32; rows of channel c and kv head h at k + row*k_token + h*k_head + c).  A page whose
  * first token is among them starts anew; any other keeps its bounds and widens them.  max_new: at
  * least the largest number of new rows of a sequence (it sizes the launch; more rows than that are
  * still taken, only slower).  block_table: device int32 [B][max_pages]; the pages of two sequences
  * that append in one call must differ.  A token past max_pages, or in a page outside [0, npages), is
- * left out.  NaN elements are skipped.
+ * left out, and a sequence whose rows are not all in [0, n) as a whole.  NaN elements are skipped.
  * Errors: TQ_ERR_INVALID_ARG (NULL pointers, bad sizes or dtype), TQ_ERR_UNSUPPORTED (D > 256, B or
  * Hkv > 65535, a pointer that is not aligned to its element), TQ_ERR_CUDA. */
-int tq_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
+int tq_page_bounds(const void* k, int64_t n, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
                    const int32_t* start, int B, int Hkv, int D, int64_t max_new, const int32_t* block_table,
                    int page_tokens, int max_pages, void* bounds, int64_t npages, tq_stream_t stream);
 
@@ -437,7 +438,8 @@ int tq_sparse_decode_attention(const tq_ctx* const* kctx, const tq_ctx* const* v
  * keys and values are in the cache already (tq_quantize_kv): they are the last n_b = draft_lens[b] of
  * sequence b's seq_lens[b] tokens.  Query row j < n_b of sequence b attends all tokens before the
  * drafted ones and drafted token i where bit i % 64 of tree_mask[b][j][i / 64] is set (its ancestors and
- * itself, for a tree; any mask is allowed).  A row that attends nothing, and every row j >= n_b, gives
+ * itself, for a tree; any mask is allowed).  A token with a norm that is not finite makes the rows that
+ * attend it NaN, and no others.  A row that attends nothing, and every row j >= n_b, gives
  * zeros.  Accepted tokens are kept by quantizing them to their final slots; nothing else in the cache
  * changes.
  * q, out: device [B][T][Hq][D] of q_dtype (F32, BF16, F16), 16-byte aligned (and channel_perm); 1 <= T <= 256.  draft_lens: device int32 [B],
@@ -461,13 +463,13 @@ int tq_tree_mask(const int32_t* parent, int B, int T, uint64_t* mask);
 
 /* Test hooks (not for production use).
  * tq_debug_set_wait_limit -- limit, in nanoseconds, of the pipeline waits of the
- *   dequantize, search and workspace-quantize kernels launched after the call (default 2 s;
+ *   dequantize, search, workspace-quantize and tree-attention kernels launched after the call (default 2 s;
  *   0 makes every wait that is not already satisfied give up at once).  Their final
  *   drains of in-flight copies and MMAs keep the 2 s limit, so a kernel that gives up still
  *   leaves no transfer behind.  Process-wide; not thread-safe against concurrent launches.
- * tq_debug_inject_stall -- while on, the dequantize kernel's MMA issuer first waits on a
- *   barrier that nothing arrives on; the wait gives up after the pipeline wait limit,
- *   records device error 305 and the kernel winds down (its output is then undefined).
+ * tq_debug_inject_stall -- while on, the dequantize and tree-attention kernels' MMA issuers first wait on
+ *   a barrier that nothing arrives on; the wait gives up after the pipeline wait limit,
+ *   records device error 305 (615) and the kernel winds down (its output is then undefined).
  * tq_debug_fail_alloc -- make device allocation number `index` (0-based, counted from this
  *   call) inside tq_init fail as if the device were out of memory; -1 disables.  tq_init
  *   then returns TQ_ERR_ALLOC having released everything it allocated. */

@@ -107,7 +107,7 @@ def lib():
         "tq_search_topk": (I, [P, P, I64, PK, I64, I, P, P, P, SZ, P]),
         "tq_rope": (I, [P, I, I, I64, I, I, P, P, I, ctypes.c_double, I, P]),
         "tq_rope_frequencies": (I, [I, ctypes.c_double, ctypes.POINTER(_RopeScaling), P, ctypes.POINTER(ctypes.c_double)]),
-        "tq_page_bounds": (I, [P, I, I64, I64, P, P, I, I, I, I64, P, I, I, P, I64, P]),
+        "tq_page_bounds": (I, [P, I64, I, I64, I64, P, P, I, I, I, I64, P, I, I, P, I64, P]),
         "tq_sparse_workspace_size": (SZ, [I, I, I, I, I, I64, I, I]),
         "tq_sparse_decode_attention": (I, [P, P, P, I, P, I, PK, PK, P, I, I, I, I, I64, F, P,
                                            ctypes.POINTER(_SparseOpts), P, SZ, P]),
@@ -502,7 +502,7 @@ def page_bounds(k, cu_new, start, block_table, page_tokens: int, bounds, max_new
     _int32(cu_new, (B + 1,), "cu_new")
     _int32(block_table, (B, block_table.shape[-1]), "block_table")
     _on_current_device(k, cu_new, start, block_table, bounds)
-    _check(lib().tq_page_bounds(k.data_ptr(), _dtype_code(k), k.stride(0), k.stride(1), cu_new.data_ptr(), start.data_ptr(),
+    _check(lib().tq_page_bounds(k.data_ptr(), k.shape[0], _dtype_code(k), k.stride(0), k.stride(1), cu_new.data_ptr(), start.data_ptr(),
                                 B, k.shape[1], k.shape[2], int(max_new), block_table.data_ptr(), int(page_tokens),
                                 block_table.shape[1], bounds.data_ptr(), bounds.shape[0], _raw_stream(stream)))
     return bounds

@@ -51,7 +51,7 @@ int launch_logits_mma(const tq_ctx* ctx, const float* q, int64_t nq, const tq_pa
 int launch_rope(const tq_rope_tensor* t, int nt, int dtype, int64_t n, int D, int rot, const double* freq,
                 const void* pos, int pos_bits, double factor, int flags, cudaStream_t st);
 int rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* freq, double* factor);
-int launch_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
+int launch_page_bounds(const void* k, int64_t n, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
                        const int32_t* start, int B, int Hkv, int D, int64_t max_new, const int32_t* table,
                        int page, int max_pages, void* bounds, int64_t npages, cudaStream_t st);
 struct SparseWs {

@@ -55,6 +55,7 @@ constexpr int kBoundThreads = 128, kBoundRows = 8, kBoundCtas = 8;   // CTAs an 
 
 struct BoundArgs {
   const void* k;
+  int64_t n;                 // its rows
   int64_t kt, kh;            // strides in elements: token, kv head
   void* bounds;              // [pages][Hkv][2][D]
   const int32_t* cu_new;     // [B + 1] first new row of every sequence
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kBoundThreads, kBoundCtas) page_bounds_kernel(
   const int b = blockIdx.z, hk = blockIdx.x % A.Hkv, first = blockIdx.x / A.Hkv, step = gridDim.x / A.Hkv;
   const int lanes = A.D / V, groups = max(1, kBoundThreads / lanes);
   const int64_t r0 = A.cu_new[b], nnew = (int64_t)A.cu_new[b + 1] - r0;
-  if (nnew <= 0) return;
+  if (nnew <= 0 || r0 < 0 || r0 + nnew > A.n) return;
   const int64_t t0 = A.start[b], t1 = t0 + nnew;
   if (t0 < 0) return;
   const int64_t last = min((t1 - 1) / A.page, (int64_t)A.max_pages - 1);
@@ -459,12 +460,12 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-int launch_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
+int launch_page_bounds(const void* k, int64_t n, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
                        const int32_t* start, int B, int Hkv, int D, int64_t max_new, const int32_t* table,
                        int page, int max_pages, void* bounds, int64_t npages, cudaStream_t st) {
   const int es = dtype == TQ_DTYPE_F32 ? 4 : 2;
   BoundArgs A{};
-  A.k = k; A.kt = k_token; A.kh = k_head; A.bounds = bounds; A.cu_new = cu_new; A.start = start; A.table = table;
+  A.k = k; A.n = n; A.kt = k_token; A.kh = k_head; A.bounds = bounds; A.cu_new = cu_new; A.start = start; A.table = table;
   A.Hkv = Hkv; A.D = D; A.page = page; A.max_pages = max_pages; A.npages = npages;
   const int vec = 16 / es;
   const bool wide = D % vec == 0 && reinterpret_cast<uintptr_t>(k) % 16 == 0 && reinterpret_cast<uintptr_t>(bounds) % 16 == 0 && k_token % vec == 0 && k_head % vec == 0;

@@ -635,20 +635,20 @@ int tq_rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* 
   return rope_frequencies(rot, base, s, freq, factor_out);
 }
 
-int tq_page_bounds(const void* k, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
+int tq_page_bounds(const void* k, int64_t n, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
                    const int32_t* start, int B, int Hkv, int D, int64_t max_new, const int32_t* block_table,
                    int page_tokens, int max_pages, void* bounds, int64_t npages, tq_stream_t stream) {
   Range range_("tq_page_bounds");
   if (bad_dtype(dtype)) return fail(TQ_ERR_INVALID_ARG, "tq_page_bounds: dtype must be F32, BF16 or F16");
-  if (B < 0 || Hkv <= 0 || D <= 0 || max_new < 0 || page_tokens <= 0 || max_pages < 0 || npages < 0)
+  if (n < 0 || B < 0 || Hkv <= 0 || D <= 0 || max_new < 0 || page_tokens <= 0 || max_pages < 0 || npages < 0)
     return fail(TQ_ERR_INVALID_ARG, "tq_page_bounds: bad sizes");
   if (D > 256 || B > 65535 || Hkv > 65535)
     return fail(TQ_ERR_UNSUPPORTED, "tq_page_bounds: D must be at most 256, B and Hkv at most 65535");
-  if (B == 0 || max_new == 0 || max_pages == 0 || npages == 0) return TQ_OK;
+  if (n == 0 || B == 0 || max_new == 0 || max_pages == 0 || npages == 0) return TQ_OK;
   if (!k || !cu_new || !start || !block_table || !bounds) return fail(TQ_ERR_INVALID_ARG, "tq_page_bounds: NULL argument");
   if (!aligned(k, elem_size(dtype)) || !aligned(bounds, elem_size(dtype)))
     return fail(TQ_ERR_UNSUPPORTED, "tq_page_bounds: a pointer is not aligned to its element");
-  return launch_page_bounds(k, dtype, k_token, k_head, cu_new, start, B, Hkv, D, max_new, block_table, page_tokens,
+  return launch_page_bounds(k, n, dtype, k_token, k_head, cu_new, start, B, Hkv, D, max_new, block_table, page_tokens,
                             max_pages, bounds, npages, (cudaStream_t)stream);
 }
 

@@ -106,6 +106,7 @@ struct TreeArgs {
   float* part;                    // [B Hkv R][nsplit][128] rotated partial results
   float2* ml;                     // [B Hkv R][nsplit] (maximum in log2, sum)
   uint64_t wait;                  // limit of a wait, in SM cycles
+  int stall;                      // test hook: the products first wait for a barrier that nothing arrives on
   int* err;
 };
 
@@ -363,7 +364,7 @@ __device__ __forceinline__ bool bar_wait2(uint64_t* a, int pa, uint64_t* b, int 
 }
 
 struct Bars {
-  uint64_t proj, klast, wfull, xfull, ofull, dfull, drain;
+  uint64_t proj, klast, wfull, xfull, ofull, dfull, drain, never;
   // of a stage: K decoded, S formed (so K is free), V decoded, O += P V done (so V and P are free), P formed
   uint64_t kfull[kStages], sfull[kStages], vfull[kStages], vempty[kStages], pfull[kStages];
 };
@@ -443,15 +444,18 @@ struct Decode {
     for (int i = set; i < n; i += kSets) {
       const int st = i % kStages, ph = i / kStages;
       const bool live = x.live;
+      // A value norm that is not finite would reach every row through 0 * V, rows that do not attend the
+      // token among them: the value counts as 0 and the key as NaN, which only the attending rows see.
+      const bool bad = (x.vn & 0x7C00u) == 0x7C00u;
       advance(x, A, b, hk, t1);
       if (!wait(&bar->sfull[st], ph + 1)) { code = 601; return false; }
-      decode_keys<PK>(x.kw, g, live ? f(x.kn) : 0.f, live ? f(x.kr) : 0.f, at0 + st * kKBytes);
+      decode_keys<PK>(x.kw, g, live ? (bad ? NAN : f(x.kn)) : 0.f, live ? f(x.kr) : 0.f, at0 + st * kKBytes);
       load_k(x, g, half);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane0) mbar_arrive(&bar->kfull[st]);
       if (!wait(&bar->vempty[st], ph + 1)) { code = 602; return false; }
-      decode_values<PV>(x.vw, g, live ? f(x.vn) : 0.f, at0 + kOffV + st * kVBytes);
+      decode_values<PV>(x.vw, g, live && !bad ? f(x.vn) : 0.f, at0 + kOffV + st * kVBytes);
       load_v(x, g, half);
       fence_proxy_async_smem();
       __syncwarp();
@@ -541,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     mbar_init(&bar->ofull, kSoftWarps);
     mbar_init(&bar->dfull, 1);
     mbar_init(&bar->drain, 1);
+    mbar_init(&bar->never, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -859,6 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   } else {
     // ------------------------------------------------------------------ products
     const uint32_t k0 = smem_u32(smem), v0 = smem_u32(smem + kOffV);
+    if (ok && A.stall && !wait_all(&bar->never, 0)) { fail(615); ok = false; }
     constexpr uint32_t id_s = idesc_f16(kRows, kTileTok, 0), id_o = idesc_f16(kRows, kTD, 0) | kMajorN;
 #pragma unroll 1
     for (int i = 0; ok && i < n + kAhead; ++i) {
@@ -1082,6 +1088,7 @@ int launch_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, 
   A.part = reinterpret_cast<float*>(ws);
   A.ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + W.ml);
   A.wait = 2 * pipeline_wait_ns();      // (1.965 GHz at most: a limit in ns is never cut short)
+  A.stall = debug_stall() ? 1 : 0;
   A.err = kctx[0]->dev_err;
   int64_t pool = INT64_MAX;
   for (int g = 0; g < G; ++g) {

@@ -15,12 +15,12 @@ D = 128
 
 
 # ------------------------------------------------------------------ refusals (no GPU: nothing is launched)
-def _bounds(k=4096, dtype=0, cu=4096, start=4096, B=1, Hkv=1, D=8, new=1, table=4096, page=64, pages=1, out=4096, np_=1):
-    return tq.lib().tq_page_bounds(k, dtype, 8, 8, cu, start, B, Hkv, D, new, table, page, pages, out, np_, None)
+def _bounds(k=4096, n=1, dtype=0, cu=4096, start=4096, B=1, Hkv=1, D=8, new=1, table=4096, page=64, pages=1, out=4096, np_=1):
+    return tq.lib().tq_page_bounds(k, n, dtype, 8, 8, cu, start, B, Hkv, D, new, table, page, pages, out, np_, None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(dtype=5), 1), (dict(B=-1), 1), (dict(Hkv=0), 1), (dict(D=0), 1), (dict(new=-1), 1), (dict(page=0), 1),
+    (dict(dtype=5), 1), (dict(n=-1), 1), (dict(B=-1), 1), (dict(Hkv=0), 1), (dict(D=0), 1), (dict(new=-1), 1), (dict(page=0), 1),
     (dict(pages=-1), 1), (dict(np_=-1), 1), (dict(D=264), 2), (dict(B=65536), 2), (dict(Hkv=65536), 2), (dict(k=0), 1),
     (dict(cu=0), 1), (dict(start=0), 1), (dict(table=0), 1), (dict(out=0), 1), (dict(k=4097, dtype=1), 2),
     (dict(out=4098), 2),
@@ -30,7 +30,7 @@ def test_bounds_refusals(kw, status):
 
 
 def test_bounds_without_work():
-    assert _bounds(B=0, k=0) == 0 and _bounds(new=0, k=0) == 0 and _bounds(pages=0, k=0) == 0 and _bounds(np_=0, k=0) == 0
+    assert _bounds(n=0, k=0) == 0 and _bounds(B=0, k=0) == 0 and _bounds(new=0, k=0) == 0 and _bounds(pages=0, k=0) == 0 and _bounds(np_=0, k=0) == 0
 
 
 def _sparse(select=4, first=1, last=1, page=64, table=4096, bounds=4096, bdtype=1, bpages=4, max_len=256, opts=True):
@@ -123,6 +123,8 @@ def test_bounds_token_by_token_and_bad_pages():
     tq.page_bounds(k, i(0, n), i(192), table, page, all_, n)           # past the table
     tq.page_bounds(k, i(5, 5), i(0), table, page, all_, n)             # no rows
     tq.page_bounds(k, i(0, n), i(-4), table, page, all_, n)            # no such token
+    tq.page_bounds(k[:n - 1], i(0, n), i(0), table, page, all_, n)     # rows that k does not have
+    tq.page_bounds(k, i(-1, 5), i(0), table, page, all_, n)
     assert torch.equal(all_, before)
     with pytest.raises(ValueError):
         tq.page_bounds(k.half(), i(0, n), i(0), table, page, all_, n)

@@ -124,6 +124,7 @@ def test_tree_matches(kind, dtype):
     (2, 2, 200, [333, 201], [200, 130], 64),             # masks of four words
     (16, 1, 9, [1000, 3], [9, 3], 256),                  # 144 rows, splits
     (6, 2, 40, [40, 41, 100], None, 0),                  # every sequence drafts T
+    (1, 1, 256, [256, 300], [256, 255], 0),              # the most drafts
 ])
 def test_tree_shapes(Hq, Hkv, T, lens, drafts, page):
     _case(2, "4", Hq, Hkv, T, lens, drafts, page=page)
@@ -207,6 +208,62 @@ def test_tree_large_and_zero_norms():
         cache.set_norms(0, 17, value=np.float16(60000.0))
         cache.set_norms(0, 20, value=np.float16(3e-5))
     _case(11, "4", 8, 2, 4, [90], [4], torch.float32, edit=edit)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["4", "2.5"])
+@pytest.mark.parametrize("which", ["key", "value"])
+def test_tree_norms_that_are_not_finite_stay_with_the_rows_that_attend_them(kind, which):
+    """Drafted tokens 2 (infinite) and 4 (NaN): only rows that attend one of them are NaN."""
+    T, lens = 6, [150]
+    m = tq.tree_mask([[-1, 0, 0, 1, 2, 3]])                        # rows 2 and 4 attend token 2, row 4 token 4 too
+    bad = [2, 4]
+
+    def edit(cache, values):
+        for t, v in zip(bad, values):
+            cache.set_norms(0, 144 + t, **{which: np.float16(v)})
+
+    out, _ = _case(17, kind, 8, 2, T, lens, [T], mask=m, edit=lambda c: edit(c, (1.0, 1.0)))
+    rng = np.random.default_rng(17)
+    cache = cacheref.Cache(rng, kind, 1, 2, lens, 150)
+    edit(cache, (np.inf, np.nan))
+    kc, vc, _ = cacheref.upload(cache, DEV)
+    q = torch.tensor(rng.standard_normal((1, T, 8, D)), device=DEV).bfloat16()
+    kctx, vctx = cacheref.contexts(kind)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    got = tq.tree_attention(kctx, vctx, cache.off, q, kc, vc, i32(150), 2, 150, 1 / math.sqrt(D), i32(T), torch.tensor(m, device=DEV))
+    fine = [0, 1, 3, 5]
+    assert torch.equal(got[0, fine], out[0, fine])
+    if which == "value":
+        assert got[0, bad].isnan().all()
+    else:
+        assert not got[0, bad].isfinite().all()
+
+
+@gpu
+def test_tree_waits_that_run_out_are_reported():
+    """The products wait for a barrier that nothing arrives on: after a millisecond the kernel gives up, says so and
+    winds down, and the next call is right again."""
+    rng = np.random.default_rng(18)
+    cache = cacheref.Cache(rng, "4", 2, 2, [500, 300], 512, 64)
+    kc, vc, table = cacheref.upload(cache, DEV)
+    kctx, vctx = cacheref.contexts("4")
+    q = torch.randn(2, 4, 8, D, device=DEV).bfloat16()
+    sl = torch.tensor([500, 300], dtype=torch.int32, device=DEV)
+    plan = tq.TreePlan(kctx, vctx, cache.off, kc, vc, 2, 4, 8, 2, D, 512, block_table=table, page_tokens=64)
+    want = plan(q, sl, None, None, 0.1)
+    torch.cuda.synchronize()
+    assert kctx[0].device_error() == 0
+    try:
+        tq.lib().tq_debug_set_wait_limit(1000000)
+        tq.lib().tq_debug_inject_stall(1)
+        plan(q, sl, None, None, 0.1)
+        torch.cuda.synchronize()
+    finally:
+        tq.lib().tq_debug_inject_stall(0)
+        tq.lib().tq_debug_set_wait_limit(2000000000)
+    assert 601 <= kctx[0].device_error() <= 615
+    assert torch.equal(plan(q, sl, None, None, 0.1), want) and kctx[0].device_error() == 0
 
 
 @gpu
