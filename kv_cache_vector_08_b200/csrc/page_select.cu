@@ -262,11 +262,16 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------------------ selection
-// CTA per (sequence, kv head): the select-th largest key by 8-bit digits (a histogram of the
-// keys that share the prefix found so far, from the highest bit in which any two keys differ on),
-// then one ordered pass that keeps the larger keys and the first of the equal ones.  Keys sit in
-// shared memory when they fit.
-constexpr int kSelThreads = 512, kSelStaged = 4096, kSelRank = 384;   // (both ways take as long at about 400 pages)
+// CTA per (sequence, kv head); keys sit in shared memory when they fit.  Two ways:
+//   few pages: every page counts the keys in front of it;
+//   many: the select-th largest key by 8-bit digits (a histogram of the keys that share the prefix found so
+//     far, from the highest bit in which any two keys differ on), then one ordered pass that keeps the larger
+//     keys and the first of the equal ones.
+// Bound: latency (the keys are a few KB).  The whole sparse step of 4 sequences x 8 kv heads took, in us,
+//   pages      64    128    192    256    512
+//   counted  27.7   28.7   30.3   31.3   40.9     (n^2 comparisons of 64 bits: several lanes a page change nothing)
+//   digits   29.5   29.8   29.8   29.9   30.3
+constexpr int kSelThreads = 512, kSelStaged = 4096, kSelRank = 160;
 
 __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_constant__ SelectArgs A) {
   extern __shared__ __align__(16) uint64_t s_key[];

@@ -204,6 +204,18 @@ def test_sparse_many_pages():
 
 
 @gpu
+@pytest.mark.parametrize("same", [False, True])
+def test_sparse_page_counts(same):
+    """Page counts around every power of two and every way of selecting, next to one another in one batch."""
+    n = [9, 16, 17, 32, 33, 64, 65, 128, 129, 255, 256, 257, 300]
+    box = None
+    if same:                                      # every score equal: the lower pages
+        pool = cacheref.Cache(np.random.default_rng(7), "3", len(n), 1, [64 * x - 5 for x in n], 64 * max(n), 64).pool
+        box = torch.ones((pool, 1, 2, D), device=DEV, dtype=torch.bfloat16)
+    _case(7, "3", len(n), 2, 1, [64 * x - 5 for x in n], 64, 8, 0 if same else 2, 1, torch.bfloat16, box=box)
+
+
+@gpu
 def test_sparse_ties_infinities_and_nan():
     """Equal scores go to the lower page; infinite bounds win or lose; a NaN score comes last."""
     page, n, Hkv = 64, 12, 1
