@@ -154,11 +154,11 @@ int launch_bounds_t(const BoundArgs& A, int vec, dim3 grid, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------ scores
-// CTA = (sequence, kv head, 32 pages), 8 warps: q+ and q- of the group are summed once into shared
-// memory; a warp takes four pages, whose bounds are all loaded before the first is summed (lanes
-// 0-15 the minima, 16-31 the maxima, 8 channels each; twice for 32-bit bounds).  Bound: HBM, 4 D
-// bytes a page and head at 16 bits, and before that the latency of the page table and the bounds.
-constexpr int kScoreThreads = 256, kScorePages = 32, kScoreWarpPages = 4;
+// CTA = (sequence, kv head, 16 `batches` pages), 4 warps: q+ and q- of the group are summed once into
+// shared memory; a warp takes four pages at a time, whose bounds are all loaded before the first is summed
+// (lanes 0-15 the minima, 16-31 the maxima, 8 channels each; twice for 32-bit bounds).  Bound: HBM, 4 D bytes
+// a page and head at 16 bits, and before that the latency of the page table and the bounds.
+constexpr int kScoreThreads = 128, kScoreCtas = 7, kScoreWarpPages = 4, kScoreBatches = 8;   // (CTAs an SM; batches at most)
 constexpr int kSelD = 128;                 // head dimension of the caches that the decode kernels read
 
 struct SelectArgs {
@@ -170,6 +170,7 @@ struct SelectArgs {
   int64_t max_len, npages, pool;   // pages of the bounds, pages of the caches
   int select, first, last;
   int staged;                // pages whose keys fit into shared memory
+  int batches;               // of four pages, for a warp of the scores
   uint64_t* key;             // [B Hkv][max_pages] order-preserving scores
   int32_t* selected;         // [B][Hkv][select] or NULL
   int32_t* vtable;           // [B Hkv][select] pages of the one-head view
@@ -191,30 +192,35 @@ __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;\
 __device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 template <typename TQ, typename TB>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ SelectArgs A) {
+__global__ void __launch_bounds__(kScoreThreads, sizeof(TB) == 4 ? 5 : kScoreCtas) page_score_kernel(const __grid_constant__ SelectArgs A) {
   __shared__ double s_q[2 * kSelD];   // sums of the heads' negative parts (for the minima), then of the positive ones
   const int hk = blockIdx.y, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   dep_launch();
-  const int n = (live_tokens(A, b) + A.page - 1) / A.page;
-  const int p0 = blockIdx.x * kScorePages + warp * kScoreWarpPages;
+  const int mine = kScoreWarpPages * A.batches;                // pages of a warp (32 at most)
+  const int p0 = (blockIdx.x * (kScoreThreads / 32) + warp) * mine;
   const int rep = A.Hq / A.Hkv;
   constexpr int kV = 16 / (int)sizeof(TB), kL = 8 / kV;       // channels a load, loads a lane
   using VT = Vec<TB, kV>;
-  // page entries of the warp's pages, then their bounds
-  int phys = -1;
-  if (lane < kScoreWarpPages && p0 + lane < n) phys = A.table[(size_t)b * A.max_pages + p0 + lane];
+  int phys = -1;                                              // of page p0 + lane
+  if (lane < mine && p0 + lane < A.max_pages) phys = A.table[(size_t)b * A.max_pages + p0 + lane];
+  const int n = (live_tokens(A, b) + A.page - 1) / A.page;
+  if (p0 + lane >= n) phys = -1;
   VT box[kScoreWarpPages][kL];
+  auto fetch = [&](int i0) {
 #pragma unroll
-  for (int i = 0; i < kScoreWarpPages; ++i) {
-    const int pg = __shfl_sync(0xffffffffu, phys, i);
-    const bool in = pg >= 0 && pg < A.npages;
-    const TB* src = static_cast<const TB*>(A.bounds) + ((size_t)(in ? pg : 0) * A.Hkv + hk) * 2 * kSelD + 8 * lane;
+    for (int i = 0; i < kScoreWarpPages; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, phys, i0 + i);
+      const bool in = pg >= 0 && pg < A.npages;
+      const TB* src = static_cast<const TB*>(A.bounds) + ((size_t)(in ? pg : 0) * A.Hkv + hk) * 2 * kSelD + 8 * lane;
 #pragma unroll
-    for (int j = 0; j < kL; ++j)
-      if (in) box[i][j] = *reinterpret_cast<const VT*>(src + j * kV);
-  }
-  if (threadIdx.x < kSelD) {
+      for (int j = 0; j < kL; ++j)
+        if (in) box[i][j] = *reinterpret_cast<const VT*>(src + j * kV);
+    }
+  };
+  fetch(0);
+  {
+    static_assert(kScoreThreads == kSelD, "a thread a channel");
     double pos = 0.0, neg = 0.0;
     const TQ* q = static_cast<const TQ*>(A.q) + ((size_t)b * A.Hq + (size_t)hk * rep) * kSelD + threadIdx.x;
 #pragma unroll 4
@@ -227,35 +233,47 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
     s_q[kSelD + threadIdx.x] = pos;
   }
   __syncthreads();
-  if (p0 < n) {
-    double q[8], s[kScoreWarpPages];
+  double q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = s_q[8 * lane + j];
+  for (int j = 0; j < 8; ++j) q[j] = s_q[8 * lane + j];
+  uint32_t keep[kL * 4];              // bits of the channels whose q is not 0: 0 * infinity is no bound
+#pragma unroll
+  for (int w = 0; w < kL * 4; ++w)
+    keep[w] = kL == 2 ? (q[w] != 0.0 ? ~0u : 0u)
+                      : (q[2 * w % 8] != 0.0 ? 0xFFFFu : 0u) | (q[(2 * w + 1) % 8] != 0.0 ? 0xFFFF0000u : 0u);
+#pragma unroll 1
+  for (int i0 = 0; i0 < mine && p0 + i0 < n; i0 += kScoreWarpPages) {
+    if (i0 > 0) fetch(i0);
+    double s[kScoreWarpPages];
 #pragma unroll
     for (int i = 0; i < kScoreWarpPages; ++i) {
-      const int pg = __shfl_sync(0xffffffffu, phys, i);
+      const int pg = __shfl_sync(0xffffffffu, phys, i0 + i);
       s[i] = 0.0;
       if (pg >= 0 && pg < A.npages) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(box[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (q[j] != 0.0) s[i] = fma(q[j], (double)to_f<TB>(box[i][j / kV].v[j % kV]), s[i]);   // (0 * infinity is no bound)
+        for (int j = 0; j < kL * 4; ++j) w[j] &= keep[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i] = fma(q[j], (double)to_f<TB>(box[i][j / kV].v[j % kV]), s[i]);
       } else {
         s[i] = -INFINITY;
       }
     }
+    // sums over the lanes: halves of the warp take two pages each, then quarters one
+    const bool up = lane & 16, up2 = lane & 8;
+    double x0 = up ? s[2] : s[0], x1 = up ? s[3] : s[1];
+    x0 += __shfl_xor_sync(0xffffffffu, up ? s[0] : s[2], 16);
+    x1 += __shfl_xor_sync(0xffffffffu, up ? s[1] : s[3], 16);
+    double x = up2 ? x1 : x0;
+    x += __shfl_xor_sync(0xffffffffu, up2 ? x0 : x1, 8);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < kScoreWarpPages; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-#pragma unroll
-    for (int i = 0; i < kScoreWarpPages; ++i) {
-      const int p = p0 + i;
-      if (lane == i && p < n) {
-        uint64_t key = order_key(s[i]);
-        if (key == ~0ull) --key;
-        if (p < A.first || p >= n - A.last) key = ~0ull;
-        A.key[((size_t)b * A.Hkv + hk) * A.max_pages + p] = key;
-      }
+    for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    const int p = p0 + i0 + (lane >> 3);
+    if ((lane & 7) == 0 && p < n) {
+      uint64_t key = order_key(x);
+      if (key == ~0ull) --key;
+      if (p < A.first || p >= n - A.last) key = ~0ull;
+      A.key[((size_t)b * A.Hkv + hk) * A.max_pages + p] = key;
     }
   }
   dep_wait();     // (the projection of the queries in front of this kernel is done when this one is)
@@ -288,6 +306,7 @@ __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_con
     const int phys = table[i];
     return phys >= 0 && phys < A.pool ? phys * A.Hkv + hk : -1;
   };
+  const int ahead = n <= kSelRank && tid < n ? view(tid) : -1;     // (on its way while the scores are formed)
   dep_wait();                        // the scores
   if (n <= A.select) {               // every page
     for (int i = tid; i < A.select; i += kSelThreads) {
@@ -322,7 +341,7 @@ __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_con
     for (int w = 0; w < warp; ++w) rank += s_warp[w][0];
     if (take) {
       if (A.selected) A.selected[(size_t)vh * A.select + rank] = tid;
-      A.vtable[(size_t)vh * A.select + rank] = view(tid);
+      A.vtable[(size_t)vh * A.select + rank] = ahead;
       if (rank == A.select - 1) A.vlen[vh] = tid == n - 1 ? (A.select - 1) * A.page + (len - tid * A.page) : A.select * A.page;
     }
     return;
@@ -512,7 +531,14 @@ int launch_page_select(const void* q, int q_dtype, const int32_t* seq_lens, int 
   A.vlen = reinterpret_cast<int32_t*>(base + W.vlen);
   int r = TQ_OK;
   if (A.max_pages > A.select) {        // (otherwise every page is read and none is scored)
-    const dim3 grid((unsigned)div_up(A.max_pages, kScorePages), (unsigned)Hkv, (unsigned)B);
+    // one wave of CTAs, each with as few pages as that allows (32 pages a CTA and several waves: 17.4 us for
+    // 64 sequences of 8 heads and 128 pages; so: 12.8 us)
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int step = kScoreWarpPages * (kScoreThreads / 32);
+    A.batches = 1;
+    while (A.batches < kScoreBatches && (int64_t)div_up(A.max_pages, step * A.batches) * Hkv * B > (int64_t)kScoreCtas * sms) ++A.batches;
+    const dim3 grid((unsigned)div_up(A.max_pages, step * A.batches), (unsigned)Hkv, (unsigned)B);
     if (q_dtype == TQ_DTYPE_F32) r = launch_score_q<float>(A, o->bounds_dtype, grid, st);
     else if (q_dtype == TQ_DTYPE_BF16) r = launch_score_q<__nv_bfloat16>(A, o->bounds_dtype, grid, st);
     else r = launch_score_q<__half>(A, o->bounds_dtype, grid, st);
