@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_con
     const int phys = table[i];
     return phys >= 0 && phys < A.pool ? phys * A.Hkv + hk : -1;
   };
-  const int ahead = n <= kSelRank && tid < n ? view(tid) : -1;     // (on its way while the scores are formed)
+  int ahead = n > A.select && tid < n ? view(tid) : -1;     // (on its way while the scores are formed)
   dep_wait();                        // the scores
   if (n <= A.select) {               // every page
     for (int i = tid; i < A.select; i += kSelThreads) {
@@ -348,10 +348,15 @@ __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_con
   }
   const bool staged = n <= A.staged;
   uint64_t all_and = ~0ull, all_or = 0;
-  for (int i = tid; i < n; i += kSelThreads) {
-    const uint64_t k = gkey[i];
-    if (staged) s_key[i] = k;
-    if (k != ~0ull) { all_and &= k; all_or |= k; }     // (the pages taken in any case have no score)
+  for (int i0 = tid; i0 < n; i0 += 4 * kSelThreads) {
+    uint64_t k[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = i0 + j * kSelThreads < n ? gkey[i0 + j * kSelThreads] : ~0ull;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (staged && i0 + j * kSelThreads < n) s_key[i0 + j * kSelThreads] = k[j];
+      if (k[j] != ~0ull) { all_and &= k[j]; all_or |= k[j]; }     // (the pages taken in any case have no score)
+    }
   }
   const uint64_t* key = staged ? s_key : gkey;
 #pragma unroll
@@ -421,7 +426,8 @@ __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_con
   }
   int base = 0, eq_base = 0;
   for (int i0 = 0; i0 < n && base < want; i0 += kSelThreads) {
-    const int i = i0 + tid;
+    const int i = i0 + tid, here = ahead;
+    if (i + kSelThreads < n) ahead = view(i + kSelThreads);
     const uint64_t k = i < n ? key[i] : 0;
     const bool must = forced < want && k == ~0ull;
     const bool gt = must || (i < n && (k & mask) > bar), eq = !gt && i < n && (k & mask) == bar;
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kSelThreads) page_pick_kernel(const __grid_con
     }
     if (take) {
       if (A.selected) A.selected[(size_t)vh * A.select + rank] = i;
-      A.vtable[(size_t)vh * A.select + rank] = view(i);
+      A.vtable[(size_t)vh * A.select + rank] = here;
       if (rank == want - 1) A.vlen[vh] = i == n - 1 ? (want - 1) * A.page + (len - i * A.page) : want * A.page;
     }
     base += all;
