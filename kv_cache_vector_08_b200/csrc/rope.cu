@@ -13,7 +13,7 @@
 // Bound: HBM (every element is read and written once).  A thread moves one vector of each
 // half of the pairs (half layout) or one vector of pairs (interleaved) at a time; queries and
 // keys go in one launch, since for a decode step the launch is the cost.  32,768 tokens of 32 + 8 heads
-// of 128 channels (bf16, 671 MB): 127 us, 5.3 TB/s, 0.81 of a copy's rate; 64 tokens: 2.4 us.
+// of 128 channels (bf16, 671 MB): 125 us, 5.4 TB/s, 0.82 of a copy's rate; 64 tokens: 2.4 us.
 #include <algorithm>
 #include <cmath>
 
@@ -79,7 +79,7 @@ struct alignas(sizeof(T) * V) Vec {
 };
 
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const __grid_constant__ RopeArgs A) {
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_constant__ RopeArgs A) {
   extern __shared__ float2 s_cs[];   // [tb][rot / 2] (cos, sin), times the factor
   using VT = Vec<T, V>;
   constexpr bool kTwo = !(INTER && V > 1);    // a unit that rotates has a vector of each half
@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const __grid_cons
     }
   };
   // The thread's first unit is on its way while the angles are formed.  (One unit at a time and many
-  // warps: four units a thread need 126 registers, and with 16 warps an SM the 32K prompt took 218 us.)
+  // warps: four units a thread need 126 registers, and with 16 warps an SM the 32K prompt took 218 us; two
+  // units, 32 warps: 134 us; one, 32 or 40 warps: 127 and 125 us; 48 spill: 127 us.)
   Unit x;
   int u = u0 + threadIdx.x;
   if (u < u1) fetch(u, x);
