@@ -6,6 +6,7 @@ first use (build it with ``python -m kv_cache_vector_08_b200.build``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -454,10 +455,10 @@ def rope(q, k, positions, freqs, *, interleaved: bool = False, factor: float = 1
     n, wide = q.shape[0], positions.dtype is torch.int64
     if not (wide or positions.dtype is torch.int32) or positions.shape != (n,) or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 or int64 tensor [n]")
-    q_out, args = _rope_side(q, q_out, q)
+    q_out, args = _rope_side(q, q_out, q, stream)
     count = 1
     if k is not None:
-        k_out, more = _rope_side(k, k_out, q)
+        k_out, more = _rope_side(k, k_out, q, stream)
         args += more
         count = 2
     _on_current_device(q, k, positions, freqs, q_out, k_out)
@@ -470,10 +471,14 @@ def rope(q, k, positions, freqs, *, interleaved: bool = False, factor: float = 1
 _ROPE_SIDES = {n: struct.Struct("@" + n * "PPi4xqqqq") for n in (1, 2)}     # tq_rope_tensor, n times
 
 
-def _rope_side(x, out, q):
+def _rope_side(x, out, q, stream):
     """(output, fields of a tq_rope_tensor) of one tensor of the call."""
     if out is None:
-        out = _torch().empty_like(x)
+        if stream is None:
+            out = _torch().empty_like(x)
+        else:
+            with _on(stream):
+                out = _torch().empty_like(x)
     shape = x.shape
     if len(shape) != 3 or shape[0] != q.shape[0] or shape[2] != q.shape[2] or out.shape != shape \
             or x.dtype is not q.dtype or out.dtype is not q.dtype:
@@ -482,6 +487,8 @@ def _rope_side(x, out, q):
     ot, oh, oc = out.stride()
     if xc != 1 or oc != 1:
         raise ValueError("q, k and their outputs must have unit stride along channels")
+    if (ot == 0 and shape[0] > 1) or (oh == 0 and shape[1] > 1):
+        raise ValueError("an output must not be expanded")
     return out, (x.data_ptr(), out.data_ptr(), shape[1], xt, xh, ot, oh)
 
 
@@ -508,6 +515,11 @@ def page_bounds(k, cu_new, start, block_table, page_tokens: int, bounds, max_new
     return bounds
 
 
+def _on(stream):
+    """Allocations and copies of a call belong to the stream that it runs on."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
 class _CachePlan:
     """Pre-marshalled caches of the calls below (as DecodePlan keeps them)."""
 
@@ -525,14 +537,22 @@ class _CachePlan:
     def _workspace(self, need):
         return _torch().empty(max(need, 1), dtype=_torch().uint8, device=self.device)
 
-    def _query(self, q, shape, out):
+    def _same_device(self, *tensors):
+        for t in tensors:
+            if t is not None and t.device != self.device:
+                raise ValueError("expected tensors on the caches' device (%s), got one on %s" % (self.device, t.device))
+
+    def _query(self, q, shape, out, stream):
         if q.shape != shape:
             raise ValueError("q must be %s, got %s" % (shape, tuple(q.shape)))
-        if not q.is_contiguous():
-            q = q.contiguous()
-        if out is None:
-            out = _torch().empty_like(q)
-        elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
+        if stream is not None:
+            self.workspace.record_stream(stream)     # (the plan may be dropped while the call runs)
+        if out is None or not q.is_contiguous():
+            with _on(stream):
+                q = q.contiguous()
+                if out is None:
+                    return q, _torch().empty_like(q)
+        if out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, with the shape and dtype of q")
         return q, out
 
@@ -555,6 +575,7 @@ class SparsePlan(_CachePlan):
         _int32(block_table, (B, max_len // page_tokens), "block_table")
         if channel_perm is not None:
             _int32(channel_perm, (Hkv, D), "channel_perm")
+        self._same_device(block_table, channel_perm)
         self.select = int(select)
         self.selected = torch.empty((B, Hkv, max(self.select, 1)), dtype=torch.int32, device=self.device)
         self._opts = _SparseOpts(0, 0, 0, self.select, int(first), int(last), self.selected.data_ptr(),
@@ -565,7 +586,9 @@ class SparsePlan(_CachePlan):
 
     def __call__(self, q, bounds, seq_lens, scale: float, out=None, stream=None):
         """q [B, Hq, D] -> (out [B, Hq, D] of q's dtype, selected int32 [B, Hkv, select]: the plan's own tensor)."""
-        q, out = self._query(q, (self.B, self.Hq, self.D), out)
+        q, out = self._query(q, (self.B, self.Hq, self.D), out, stream)
+        if stream is not None:
+            self.selected.record_stream(stream)
         if bounds.dim() != 4 or bounds.shape[1:] != (self.Hkv, 2, self.D) or not bounds.is_contiguous():
             raise ValueError("bounds must be contiguous [pages, Hkv, 2, D]")
         _int32(seq_lens, (self.B,), "seq_lens")
@@ -583,8 +606,9 @@ def sparse_decode_attention(kctx, vctx, group_off, q, bounds, kcache, vcache, se
                             block_table, page_tokens, select, first=1, last=1, out=None, stream=None, channel_perm=None):
     """One decode step over the pages that their key bounds select -> (out, selected); see tq.h."""
     B, Hq, D = q.shape
-    plan = SparsePlan(kctx, vctx, group_off, kcache, vcache, B, Hq, Hkv, D, max_len, block_table=block_table,
-                      page_tokens=page_tokens, select=select, first=first, last=last, channel_perm=channel_perm)
+    with _on(stream):
+        plan = SparsePlan(kctx, vctx, group_off, kcache, vcache, B, Hq, Hkv, D, max_len, block_table=block_table,
+                          page_tokens=page_tokens, select=select, first=first, last=last, channel_perm=channel_perm)
     return plan(q, bounds, seq_lens, scale, out, stream)
 
 
@@ -620,6 +644,7 @@ class TreePlan(_CachePlan):
             _int32(block_table, (B, max_len // page_tokens), "block_table")
         if channel_perm is not None:
             _int32(channel_perm, (Hkv, D), "channel_perm")
+        self._same_device(block_table, channel_perm)
         self._opts = _DecodeOpts(0 if channel_perm is None else channel_perm.data_ptr(),
                                  0 if block_table is None else block_table.data_ptr(), int(page_tokens))
         self._keep_opts = (channel_perm, block_table)
@@ -629,7 +654,7 @@ class TreePlan(_CachePlan):
         """q [B, T, Hq, D] -> out of its shape and dtype.  draft_lens int32 [B] or None (T each); mask int64
         [B, T, ceil(T / 64)] (tree_mask) or None (a chain)."""
         torch = _torch()
-        q, out = self._query(q, (self.B, self.T, self.Hq, self.D), out)
+        q, out = self._query(q, (self.B, self.T, self.Hq, self.D), out, stream)
         _int32(seq_lens, (self.B,), "seq_lens")
         if draft_lens is not None:
             _int32(draft_lens, (self.B,), "draft_lens")
@@ -649,6 +674,7 @@ def tree_attention(kctx, vctx, group_off, q, kcache, vcache, seq_lens, Hkv, max_
     """Attention of T drafted tokens per sequence, the last ones of its cache, under a tree mask; q [B, T, Hq, D] -> out
     of its shape and dtype (see tq.h)."""
     B, T, Hq, D = q.shape
-    plan = TreePlan(kctx, vctx, group_off, kcache, vcache, B, T, Hq, Hkv, D, max_len, channel_perm=channel_perm,
-                    block_table=block_table, page_tokens=page_tokens)
+    with _on(stream):
+        plan = TreePlan(kctx, vctx, group_off, kcache, vcache, B, T, Hq, Hkv, D, max_len, channel_perm=channel_perm,
+                        block_table=block_table, page_tokens=page_tokens)
     return plan(q, seq_lens, draft_lens, mask, scale, out, stream)

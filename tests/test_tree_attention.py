@@ -298,6 +298,44 @@ def test_tree_bad_page_is_reported():
 
 
 @gpu
+def test_calls_on_another_stream_own_what_they_allocate():
+    """Queries that are not contiguous, outputs and workspaces of calls on a side stream, with the current stream
+    busy reusing memory at the same time; tables on the host are refused before anything runs."""
+    rng = np.random.default_rng(24)
+    cache = cacheref.Cache(rng, "4", 2, 2, [200, 90], 256, 64)
+    kc, vc, table = cacheref.upload(cache, DEV)
+    kctx, vctx = cacheref.contexts("4")
+    wide = torch.randn(2, 5, 8, 2 * D, device=DEV).bfloat16()
+    q, q1 = wide[..., :D], wide[:, 0, :, D:]
+    box = torch.randn(cache.pool, 2, 2, D, device=DEV).bfloat16().sort(2).values
+    sl = torch.tensor([200, 90], dtype=torch.int32, device=DEV)
+    args = (kctx, vctx, cache.off)
+    tree = lambda **kw: tq.tree_attention(*args, q, kc, vc, sl, 2, 256, 0.1, block_table=table, page_tokens=64, **kw)  # noqa: E731
+    sparse = lambda **kw: tq.sparse_decode_attention(*args, q1, box, kc, vc, sl, 2, 256, 0.1, block_table=table,  # noqa: E731
+                                                     page_tokens=64, select=2, **kw)
+    pos, f = torch.arange(10, device=DEV), torch.ones(64, dtype=torch.float64, device=DEV)
+    rows = wide.reshape(10, 8, 2 * D)[..., :D]
+    want_t, (want_s, want_p), (want_r, _) = tree(), sparse(), tq.rope(rows, None, pos, f)
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        side.wait_stream(torch.cuda.current_stream())
+        t, (s, p), (r, _) = tree(stream=side), sparse(stream=side), tq.rope(rows, None, pos, f, stream=side)
+        for _ in range(4):
+            torch.full((1 << 16,), float("nan"), device=DEV)
+            torch.full((2, 5, 8, D), float("nan"), device=DEV, dtype=torch.bfloat16)
+        side.synchronize()
+        assert torch.equal(t, want_t) and torch.equal(s, want_s) and torch.equal(p, want_p) and torch.equal(r, want_r)
+    with pytest.raises(ValueError):
+        tq.tree_attention(*args, q, kc, vc, sl, 2, 256, 0.1, block_table=table.cpu(), page_tokens=64)
+    with pytest.raises(ValueError):
+        tq.sparse_decode_attention(*args, q1, box, kc, vc, sl, 2, 256, 0.1, block_table=table.cpu(), page_tokens=64, select=2)
+    with pytest.raises(ValueError):
+        tree(channel_perm=torch.arange(D, dtype=torch.int32).repeat(2, 1))
+    with pytest.raises(ValueError):
+        tq.rope(rows, None, pos, f, q_out=torch.empty(10, 1, D, device=DEV, dtype=torch.bfloat16).expand(10, 8, D))
+
+
+@gpu
 def test_tree_plan_streams_graphs_and_refusals():
     rng = np.random.default_rng(14)
     cache = cacheref.Cache(rng, "4", 2, 2, [200, 90], 256, 64)
