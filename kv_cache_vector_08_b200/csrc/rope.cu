@@ -24,6 +24,7 @@ namespace tq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeRowBytes = 16 * 1024;   // of whole rows in a block's shared memory
 constexpr int64_t kRopeMaxRow = 1 << 19;   // elements of one token over both tensors
 
 // n / d for n d < 2^40, n < 2^20 by one multiplication
@@ -48,7 +49,8 @@ struct RopeArgs {
   int tb;                   // tokens per block
   int per_block;            // units of a block (tb * heads * units)
   int chunk;                // units per grid.y slice
-  Div per_tok, per_head;    // units of a token, units of a head
+  Div per_tok, per_head;    // units of a token, units of a head (whole rows: rows of a token, pieces of a row)
+  Div per_row;              // pairs of a row
   int rot_units;            // units of a head that rotate (the others copy)
   const double* freq;
   const void* pos;
@@ -77,6 +79,26 @@ template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
   T v[V];
 };
+
+// (written out, so that every kernel rounds alike)
+__device__ __forceinline__ void turn_pair(float x1, float x2, float2 w, float& y1, float& y2) {
+  y1 = fmaf(x1, w.x, -(x2 * w.y));
+  y2 = fmaf(x2, w.x, x1 * w.y);
+}
+
+// Cosines and sines, times the factor, of tokens t0 .. t0 + ntok - 1.
+__device__ __forceinline__ void form_angles(const RopeArgs& A, int64_t t0, int ntok, float2* cs) {
+  const int np = A.rot / 2;
+  for (int e = threadIdx.x; e < ntok * np; e += kRopeThreads) {
+    const int t = e / np, i = e - t * np;
+    const double pos = A.pos64 ? (double)static_cast<const int64_t*>(A.pos)[t0 + t]
+                               : (double)static_cast<const int32_t*>(A.pos)[t0 + t];
+    const double turns = pos * (A.freq[i] * 0.15915494309189533577);
+    float si, co;
+    sincospif((float)(2.0 * (turns - rint(turns))), &si, &co);
+    cs[e] = make_float2(co * A.factor, si * A.factor * A.sign);
+  }
+}
 
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_constant__ RopeArgs A) {
@@ -125,8 +147,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
       for (int j = 0; j < V; ++j) {
         const float2 w = cs[x.k * V + j];
         const float x1 = to_f<T>(x.a.v[j]), x2 = to_f<T>(x.b.v[j]);
-        x.a.v[j] = from_f<T>(x1 * w.x - x2 * w.y);
-        x.b.v[j] = from_f<T>(x2 * w.x + x1 * w.y);
+        float y1, y2;
+        turn_pair(x1, x2, w, y1, y2);
+        x.a.v[j] = from_f<T>(y1);
+        x.b.v[j] = from_f<T>(y2);
       }
       *reinterpret_cast<VT*>(x.o + (INTER ? 2 * x.k : x.k * V)) = x.a;
       *reinterpret_cast<VT*>(x.o + (INTER ? 2 * x.k + 1 : x.k * V + np)) = x.b;
@@ -135,8 +159,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
       for (int j = 0; j < V / 2; ++j) {
         const float2 w = cs[x.k * (V / 2) + j];
         const float x1 = to_f<T>(x.a.v[2 * j]), x2 = to_f<T>(x.a.v[2 * j + 1]);
-        x.a.v[2 * j] = from_f<T>(x1 * w.x - x2 * w.y);
-        x.a.v[2 * j + 1] = from_f<T>(x2 * w.x + x1 * w.y);
+        float y1, y2;
+        turn_pair(x1, x2, w, y1, y2);
+        x.a.v[2 * j] = from_f<T>(y1);
+        x.a.v[2 * j + 1] = from_f<T>(y2);
       }
       *reinterpret_cast<VT*>(x.o + x.k * V) = x.a;
     }
@@ -147,21 +173,82 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
   Unit x;
   int u = u0 + threadIdx.x;
   if (u < u1) fetch(u, x);
-  for (int e = threadIdx.x; e < ntok * np; e += kRopeThreads) {
-    const int t = e / np, i = e - t * np;
-    const double pos = A.pos64 ? (double)static_cast<const int64_t*>(A.pos)[t0 + t]
-                               : (double)static_cast<const int32_t*>(A.pos)[t0 + t];
-    const double turns = pos * (A.freq[i] * 0.15915494309189533577);
-    float si, co;
-    sincospif((float)(2.0 * (turns - rint(turns))), &si, &co);
-    s_cs[e] = make_float2(co * A.factor, si * A.factor * A.sign);
-  }
+  form_angles(A, t0, ntok, s_cs);
   __syncthreads();
   while (u < u1) {
     turn(x);
     u += kRopeThreads;
     if (u < u1) fetch(u, x);
   }
+}
+
+// The same where the halves are no multiples of 16 bytes but whole rows are (a row: one head of one token): rows
+// come to shared memory 16 bytes at a time, turn there pair by pair, and go out 16 bytes at a time.
+// 16,384 tokens of 32 + 8 heads of 128 channels, 50 of them turning (bf16, 336 MB): 77 us, 0.67 of a copy's rate;
+// the kernel above with its narrow pieces takes 333 us (interleaved 215 us, 52 channels 177 us).  Rows whose halves
+// are multiples of 16 bytes stay with the kernel above: 66 us where this one takes 101 us.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeArgs A) {
+  extern __shared__ __align__(16) uint8_t s_rows[];   // [chunk][D], then [tb][rot / 2] (cos, sin)
+  T* rows = reinterpret_cast<T*>(s_rows);
+  float2* s_cs = reinterpret_cast<float2*>(s_rows + (size_t)A.chunk * A.D * sizeof(T));
+  constexpr int V = 16 / (int)sizeof(T);
+  const int64_t t0 = (int64_t)blockIdx.x * A.tb;
+  const int ntok = (int)(A.n - t0 < A.tb ? A.n - t0 : A.tb), np = A.rot / 2;
+  const int r0 = blockIdx.y * A.chunk, nrow = min(A.chunk, ntok * A.per_tok.d - r0);    // rows of the block's tokens
+  // element 16-byte piece e of the block's rows is at
+  auto piece = [&](int e, bool out) -> uint8_t* {
+    const int r = A.per_head.quot(e), c = e - r * A.per_head.d, t = A.per_tok.quot(r0 + r);
+    int h = r0 + r - t * A.per_tok.d;
+    const bool second = h >= A.heads0;
+    h -= second ? A.heads0 : 0;
+    const int64_t at = out ? (t0 + t) * (second ? A.s[1].ot : A.s[0].ot) + h * (second ? A.s[1].oh : A.s[0].oh)
+                           : (t0 + t) * (second ? A.s[1].xt : A.s[0].xt) + h * (second ? A.s[1].xh : A.s[0].xh);
+    const void* base = out ? (second ? A.s[1].out : A.s[0].out) : (second ? A.s[1].x : A.s[0].x);
+    return const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) + (at + c * V) * (int64_t)sizeof(T);
+  };
+  for (int e = threadIdx.x; e < nrow * A.per_head.d; e += kRopeThreads)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(s_rows + (size_t)e * 16)),
+                 "l"(piece(e, false)) : "memory");
+  form_angles(A, t0, ntok, s_cs);
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
+  __syncthreads();
+  for (int e = threadIdx.x; e < nrow * np; e += kRopeThreads) {
+    const int r = A.per_row.quot(e), i = e - r * np;
+    T* x = rows + r * A.D + (INTER ? 2 * i : i);
+    T* z = x + (INTER ? 1 : np);
+    float y1, y2;
+    turn_pair(to_f<T>(*x), to_f<T>(*z), s_cs[A.per_tok.quot(r0 + r) * np + i], y1, y2);
+    *x = from_f<T>(y1);
+    *z = from_f<T>(y2);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < nrow * A.per_head.d; e += kRopeThreads)
+    *reinterpret_cast<uint4*>(piece(e, true)) = *reinterpret_cast<const uint4*>(s_rows + (size_t)e * 16);
+}
+
+template <typename T>
+int launch_rows(RopeArgs A, int heads, bool inter, int sms, cudaStream_t st) {
+  A.per_head = Div(A.D * (int)sizeof(T) / 16);
+  A.per_tok = Div(heads);
+  A.per_row = Div(A.rot / 2);
+  const int most = std::max(1, kRopeRowBytes / (A.D * (int)sizeof(T)));       // rows a block
+  int64_t tb = std::max<int64_t>(1, most / heads);
+  tb = std::max<int64_t>(1, std::min<int64_t>(tb, A.n / (4 * sms)));
+  tb = std::min<int64_t>(tb, std::max(1, 16 * 1024 / (A.rot / 2 * (int)sizeof(float2))));
+  A.tb = (int)tb;
+  const int64_t blocks = (A.n + tb - 1) / tb;
+  const int rows = A.tb * heads;
+  int64_t slices = (rows + most - 1) / most;
+  if (blocks * slices < 2 * sms) slices = std::min<int64_t>((2 * sms + blocks - 1) / blocks, rows);
+  A.chunk = (int)((rows + slices - 1) / slices);
+  slices = (rows + A.chunk - 1) / A.chunk;
+  const dim3 grid((unsigned)blocks, (unsigned)slices);
+  const size_t sm = (size_t)A.chunk * A.D * sizeof(T) + (size_t)A.tb * (A.rot / 2) * sizeof(float2);
+  if (inter) rope_rows_kernel<T, true><<<grid, kRopeThreads, sm, st>>>(A);
+  else rope_rows_kernel<T, false><<<grid, kRopeThreads, sm, st>>>(A);
+  count_launch();
+  return check_launch("rope_rows_kernel");
 }
 
 template <typename T, int V>
@@ -192,7 +279,8 @@ int launch_v(RopeArgs A, int heads, bool inter, int sms, cudaStream_t st) {
 }
 
 template <typename T>
-int launch_t(const RopeArgs& A, int heads, bool inter, int vec, int sms, cudaStream_t st) {
+int launch_t(const RopeArgs& A, int heads, bool inter, int vec, bool rows, int sms, cudaStream_t st) {
+  if (rows) return launch_rows<T>(A, heads, inter, sms, st);
   if constexpr (sizeof(T) == 2)
     if (vec >= 8) return launch_v<T, 8>(A, heads, inter, sms, st);
   if (vec >= 4) return launch_v<T, 4>(A, heads, inter, sms, st);
@@ -211,6 +299,8 @@ int launch_rope(const tq_rope_tensor* t, int nt, int dtype, int64_t n, int D, in
   // widest vector that divides the rotating halves (or pairs) and the copied rest, and that
   // every pointer and stride is aligned to
   int vec = 16 / es;
+  bool rows = D % vec == 0;               // whole rows in pieces of 16 bytes
+  const int full = vec;
   auto fit = [&](int64_t elems) { while (vec > 1 && elems % vec != 0) vec /= 2; };
   auto fit_ptr = [&](const void* p) { while (vec > 1 && reinterpret_cast<uintptr_t>(p) % ((size_t)vec * es) != 0) vec /= 2; };
   fit(inter ? rot : rot / 2);
@@ -223,12 +313,15 @@ int launch_rope(const tq_rope_tensor* t, int nt, int dtype, int64_t n, int D, in
     s = RopeSide{t[i].x, t[i].out, t[i].x_token, t[i].x_head, t[i].out_token, t[i].out_head};
     if (at == 1) A.heads0 = t[i].heads;
     heads += t[i].heads;
+    rows = rows && reinterpret_cast<uintptr_t>(s.x) % 16 == 0 && reinterpret_cast<uintptr_t>(s.out) % 16 == 0 &&
+           (n <= 1 || (s.xt % full == 0 && s.ot % full == 0)) && (t[i].heads <= 1 || (s.xh % full == 0 && s.oh % full == 0));
     fit_ptr(s.x);
     fit_ptr(s.out);
     for (int64_t v : {s.xt, s.ot}) if (n > 1) fit(v);
     for (int64_t v : {s.xh, s.oh}) if (t[i].heads > 1) fit(v);
   }
   if (at == 0) return TQ_OK;
+  rows = rows && vec < full;
   if ((int64_t)heads * D > kRopeMaxRow)
     return fail(TQ_ERR_UNSUPPORTED, "tq_rope: one token has more than 2^19 elements");
   A.n = n; A.rot = rot; A.D = D; A.freq = freq; A.pos = pos; A.pos64 = pos_bits == 64;
@@ -238,9 +331,9 @@ int launch_rope(const tq_rope_tensor* t, int nt, int dtype, int64_t n, int D, in
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "tq_rope: device query");
-  if (dtype == TQ_DTYPE_F32) return launch_t<float>(A, heads, inter, vec, sms, st);
-  if (dtype == TQ_DTYPE_BF16) return launch_t<__nv_bfloat16>(A, heads, inter, vec, sms, st);
-  return launch_t<__half>(A, heads, inter, vec, sms, st);
+  if (dtype == TQ_DTYPE_F32) return launch_t<float>(A, heads, inter, vec, rows, sms, st);
+  if (dtype == TQ_DTYPE_BF16) return launch_t<__nv_bfloat16>(A, heads, inter, vec, rows, sms, st);
+  return launch_t<__half>(A, heads, inter, vec, rows, sms, st);
 }
 
 // Frequencies of the usual long-context rules (host, 64 bits).
