@@ -352,7 +352,7 @@ int tq_search_topk(const tq_ctx* ctx, const float* q, int64_t nq, const tq_packe
  *   c of head h of token v at x + v*x_token + h*x_head + c (elements; channels are contiguous).
  *   out may be x with the same strides; any other overlap is undefined.
  * freq: device double [rot/2]; pos: device int32 or int64 [n] (pos_bits 32 or 64).
- * Speed: 16-byte aligned pointers and strides, with rot/2 (rot when interleaved) and D - rot
+ * Speed: 16-byte aligned pointers and strides, with rot/2 and D - rot
  *   multiples of 16 bytes, move 16 bytes a thread; other calls give the same results with
  *   narrower ones.
  * Errors: TQ_ERR_INVALID_ARG (NULL pointers, negative sizes, rot odd or outside [2, D], bad dtype,

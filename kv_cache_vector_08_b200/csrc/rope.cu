@@ -11,7 +11,7 @@
 // block, in shared memory, and serve all heads of both tensors.
 //
 // Bound: HBM (every element is read and written once).  A thread moves one vector of each
-// half of the pairs (half layout) or one vector of pairs (interleaved) at a time; queries and
+// half of the pairs (half layout) or two adjacent ones (interleaved) at a time; queries and
 // keys go in one launch, since for a decode step the launch is the cost.  32,768 tokens of 32 + 8 heads
 // of 128 channels (bf16, 671 MB): 125 us, 5.4 TB/s, 0.82 of a copy's rate; 64 tokens: 2.4 us.
 #include <algorithm>
@@ -104,7 +104,6 @@ template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_constant__ RopeArgs A) {
   extern __shared__ float2 s_cs[];   // [tb][rot / 2] (cos, sin), times the factor
   using VT = Vec<T, V>;
-  constexpr bool kTwo = !(INTER && V > 1);    // a unit that rotates has a vector of each half
   const int64_t t0 = (int64_t)blockIdx.x * A.tb;
   const int ntok = (int)(A.n - t0 < A.tb ? A.n - t0 : A.tb), np = A.rot / 2;
   const int u0 = blockIdx.y * A.chunk, u1 = min(u0 + A.chunk, ntok * A.per_tok.d);
@@ -128,12 +127,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
           (t0 + x.t) * (second ? A.s[1].ot : A.s[0].ot) + h * (second ? A.s[1].oh : A.s[0].oh);
     if (x.k >= A.rot_units) {
       x.a = *reinterpret_cast<const VT*>(p + A.rot + (x.k - A.rot_units) * V);
-    } else if constexpr (kTwo) {
-      // V pairs: vectors of both halves, or (interleaved without alignment) one pair
-      x.a = *reinterpret_cast<const VT*>(p + (INTER ? 2 * x.k : x.k * V));
-      x.b = *reinterpret_cast<const VT*>(p + (INTER ? 2 * x.k + 1 : x.k * V + np));
     } else {
-      x.a = *reinterpret_cast<const VT*>(p + x.k * V);
+      // V pairs: vectors of both halves, or (interleaved) two adjacent ones
+      x.a = *reinterpret_cast<const VT*>(p + (INTER ? 2 * V : V) * x.k);
+      x.b = *reinterpret_cast<const VT*>(p + (INTER ? 2 * V * x.k + V : V * x.k + np));
     }
   };
   auto turn = [&](Unit& x) {
@@ -141,31 +138,19 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
       *reinterpret_cast<VT*>(x.o + A.rot + (x.k - A.rot_units) * V) = x.a;
       return;
     }
-    const float2* cs = s_cs + x.t * np;
-    if constexpr (kTwo) {
+    const float2* cs = s_cs + x.t * np + V * x.k;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 w = cs[x.k * V + j];
-        const float x1 = to_f<T>(x.a.v[j]), x2 = to_f<T>(x.b.v[j]);
-        float y1, y2;
-        turn_pair(x1, x2, w, y1, y2);
-        x.a.v[j] = from_f<T>(y1);
-        x.b.v[j] = from_f<T>(y2);
-      }
-      *reinterpret_cast<VT*>(x.o + (INTER ? 2 * x.k : x.k * V)) = x.a;
-      *reinterpret_cast<VT*>(x.o + (INTER ? 2 * x.k + 1 : x.k * V + np)) = x.b;
-    } else {
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float2 w = cs[x.k * (V / 2) + j];
-        const float x1 = to_f<T>(x.a.v[2 * j]), x2 = to_f<T>(x.a.v[2 * j + 1]);
-        float y1, y2;
-        turn_pair(x1, x2, w, y1, y2);
-        x.a.v[2 * j] = from_f<T>(y1);
-        x.a.v[2 * j + 1] = from_f<T>(y2);
-      }
-      *reinterpret_cast<VT*>(x.o + x.k * V) = x.a;
+    for (int j = 0; j < V; ++j) {
+      // pair j: elements j of the vectors, or (interleaved) elements 2 j and 2 j + 1 of both in a row
+      T& y = INTER ? (2 * j < V ? x.a.v[2 * j % V] : x.b.v[2 * j % V]) : x.a.v[j];
+      T& z = INTER ? (2 * j + 1 < V ? x.a.v[(2 * j + 1) % V] : x.b.v[(2 * j + 1) % V]) : x.b.v[j];
+      float y1, y2;
+      turn_pair(to_f<T>(y), to_f<T>(z), cs[j], y1, y2);
+      y = from_f<T>(y1);
+      z = from_f<T>(y2);
     }
+    *reinterpret_cast<VT*>(x.o + (INTER ? 2 * V : V) * x.k) = x.a;
+    *reinterpret_cast<VT*>(x.o + (INTER ? 2 * V * x.k + V : V * x.k + np)) = x.b;
   };
   // The thread's first unit is on its way while the angles are formed.  (One unit at a time and many
   // warps: four units a thread need 126 registers, and with 16 warps an SM the 32K prompt took 218 us; two
@@ -253,7 +238,7 @@ int launch_rows(RopeArgs A, int heads, bool inter, int sms, cudaStream_t st) {
 
 template <typename T, int V>
 int launch_v(RopeArgs A, int heads, bool inter, int sms, cudaStream_t st) {
-  A.rot_units = inter ? (V > 1 ? A.rot / V : A.rot / 2) : A.rot / 2 / V;
+  A.rot_units = A.rot / 2 / V;
   const int per_head = A.rot_units + (A.D - A.rot) / V;
   A.per_head = Div(per_head);
   A.per_tok = Div(per_head * heads);
@@ -296,16 +281,15 @@ int launch_rope(const tq_rope_tensor* t, int nt, int dtype, int64_t n, int D, in
   const bool inter = (flags & TQ_ROPE_INTERLEAVED) != 0;
   RopeArgs A{};
   int heads = 0;
-  // widest vector that divides the rotating halves (or pairs) and the copied rest, and that
+  // widest vector that divides the rotating halves and the copied rest, and that
   // every pointer and stride is aligned to
   int vec = 16 / es;
   bool rows = D % vec == 0;               // whole rows in pieces of 16 bytes
   const int full = vec;
   auto fit = [&](int64_t elems) { while (vec > 1 && elems % vec != 0) vec /= 2; };
   auto fit_ptr = [&](const void* p) { while (vec > 1 && reinterpret_cast<uintptr_t>(p) % ((size_t)vec * es) != 0) vec /= 2; };
-  fit(inter ? rot : rot / 2);
+  fit(rot / 2);
   fit(D - rot);
-  fit(rot);
   int at = 0;
   for (int i = 0; i < nt; ++i) {
     if (t[i].heads == 0) continue;
