@@ -13,7 +13,7 @@
 // Bound: HBM (every element is read and written once).  A thread moves one vector of each
 // half of the pairs (half layout) or two adjacent ones (interleaved) at a time; queries and
 // keys go in one launch, since for a decode step the launch is the cost.  32,768 tokens of 32 + 8 heads
-// of 128 channels (bf16, 671 MB): 125 us, 5.4 TB/s, 0.82 of a copy's rate; 64 tokens: 2.4 us.
+// of 128 channels (bf16, 671 MB): 115 us, 5.8 TB/s, 0.89 of a copy's rate; 64 tokens: 2.4 us.
 #include <algorithm>
 #include <cmath>
 
@@ -86,7 +86,15 @@ __device__ __forceinline__ void turn_pair(float x1, float x2, float2 w, float& y
   y2 = fmaf(x2, w.x, x1 * w.y);
 }
 
-// Cosines and sines, times the factor, of tokens t0 .. t0 + ntok - 1.
+// Cosines and sines, times the factor, of tokens t0 .. t0 + ntok - 1.  Units of eight pairs read them two at a time
+// from an order in which pairs 2 m and 2 m + 1 of all units are neighbours; in the order of the pairs the lanes'
+// reads met in four banks (16,384 tokens of 40 heads, bf16: 66 us instead of 61).  Units of four (32-bit types) gain
+// nothing from it (5,001 tokens of 15 heads of 96, 40 turning: 12.6 us, 12.0 in the plain order).
+template <int V>
+__device__ __forceinline__ int angle_slot(int np, int k, int j) {
+  return V < 8 ? V * k + j : ((j >> 1) * (np / V) + k) * 2 + (j & 1);
+}
+template <int V>
 __device__ __forceinline__ void form_angles(const RopeArgs& A, int64_t t0, int ntok, float2* cs) {
   const int np = A.rot / 2;
   for (int e = threadIdx.x; e < ntok * np; e += kRopeThreads) {
@@ -96,13 +104,13 @@ __device__ __forceinline__ void form_angles(const RopeArgs& A, int64_t t0, int n
     const double turns = pos * (A.freq[i] * 0.15915494309189533577);
     float si, co;
     sincospif((float)(2.0 * (turns - rint(turns))), &si, &co);
-    cs[e] = make_float2(co * A.factor, si * A.factor * A.sign);
+    cs[t * np + angle_slot<V>(np, i / V, i % V)] = make_float2(co * A.factor, si * A.factor * A.sign);
   }
 }
 
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_constant__ RopeArgs A) {
-  extern __shared__ float2 s_cs[];   // [tb][rot / 2] (cos, sin), times the factor
+  extern __shared__ __align__(16) float2 s_cs[];   // [tb][rot / 2] (cos, sin), times the factor
   using VT = Vec<T, V>;
   const int64_t t0 = (int64_t)blockIdx.x * A.tb;
   const int ntok = (int)(A.n - t0 < A.tb ? A.n - t0 : A.tb), np = A.rot / 2;
@@ -138,14 +146,17 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
       *reinterpret_cast<VT*>(x.o + A.rot + (x.k - A.rot_units) * V) = x.a;
       return;
     }
-    const float2* cs = s_cs + x.t * np + V * x.k;
+    const float2* cs = s_cs + x.t * np;
+    float4 two;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
+      if (V >= 8 && j % 2 == 0) two = *reinterpret_cast<const float4*>(cs + angle_slot<V>(np, x.k, j));
+      const float2 w = V < 8 ? cs[angle_slot<V>(np, x.k, j)] : j % 2 ? make_float2(two.z, two.w) : make_float2(two.x, two.y);
       // pair j: elements j of the vectors, or (interleaved) elements 2 j and 2 j + 1 of both in a row
       T& y = INTER ? (2 * j < V ? x.a.v[2 * j % V] : x.b.v[2 * j % V]) : x.a.v[j];
       T& z = INTER ? (2 * j + 1 < V ? x.a.v[(2 * j + 1) % V] : x.b.v[(2 * j + 1) % V]) : x.b.v[j];
       float y1, y2;
-      turn_pair(to_f<T>(y), to_f<T>(z), cs[j], y1, y2);
+      turn_pair(to_f<T>(y), to_f<T>(z), w, y1, y2);
       y = from_f<T>(y1);
       z = from_f<T>(y2);
     }
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
   Unit x;
   int u = u0 + threadIdx.x;
   if (u < u1) fetch(u, x);
-  form_angles(A, t0, ntok, s_cs);
+  form_angles<V>(A, t0, ntok, s_cs);
   __syncthreads();
   while (u < u1) {
     turn(x);
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
 // come to shared memory 16 bytes at a time, turn there pair by pair, and go out 16 bytes at a time.
 // 16,384 tokens of 32 + 8 heads of 128 channels, 50 of them turning (bf16, 336 MB): 77 us, 0.67 of a copy's rate;
 // the kernel above with its narrow pieces takes 333 us (interleaved 215 us, 52 channels 177 us).  Rows whose halves
-// are multiples of 16 bytes stay with the kernel above: 66 us where this one takes 101 us.
+// are multiples of 16 bytes stay with the kernel above: 61 us where this one takes 101 us.
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeArgs A) {
   extern __shared__ __align__(16) uint8_t s_rows[];   // [chunk][D], then [tb][rot / 2] (cos, sin)
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   for (int e = threadIdx.x; e < nrow * A.per_head.d; e += kRopeThreads)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(s_rows + (size_t)e * 16)),
                  "l"(piece(e, false)) : "memory");
-  form_angles(A, t0, ntok, s_cs);
+  form_angles<1>(A, t0, ntok, s_cs);
   asm volatile("cp.async.wait_all;\n" ::: "memory");
   __syncthreads();
   for (int e = threadIdx.x; e < nrow * np; e += kRopeThreads) {
