@@ -352,9 +352,8 @@ int tq_search_topk(const tq_ctx* ctx, const float* q, int64_t nq, const tq_packe
  *   c of head h of token v at x + v*x_token + h*x_head + c (elements; channels are contiguous).
  *   out may be x with the same strides; any other overlap is undefined.
  * freq: device double [rot/2]; pos: device int32 or int64 [n] (pos_bits 32 or 64).
- * Speed: 16-byte aligned pointers and strides, with rot/2 and D - rot
- *   multiples of 16 bytes, move 16 bytes a thread; other calls give the same results with
- *   narrower ones.
+ * Speed: 16-byte aligned pointers and strides, with D (and best rot/2) a multiple of 16 bytes,
+ *   move 16 bytes a thread; other calls give the same results with narrower accesses.
  * Errors: TQ_ERR_INVALID_ARG (NULL pointers, negative sizes, rot odd or outside [2, D], bad dtype,
  *   pos_bits or flags), TQ_ERR_UNSUPPORTED (D > 4096, more than 2^19 elements a token, a pointer
  *   that is not aligned to its element), TQ_ERR_CUDA. */

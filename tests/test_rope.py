@@ -167,6 +167,37 @@ def test_rope_strided_unaligned_and_in_place(dtype, shift):
 
 
 @gpu
+@pytest.mark.parametrize("n,Hq,Hkv,D,rot,dtype,inter", [
+    (1, 1, 0, 8, 2, torch.bfloat16, False),          # one row of one piece
+    (5, 32, 8, 128, 50, torch.bfloat16, False),
+    (2500, 6, 2, 80, 54, torch.float16, True),       # several tokens a block, a ragged last one
+    (700, 28, 4, 96, 90, torch.float32, False),
+    (3, 200, 56, 256, 250, torch.bfloat16, True),    # a token in several slices
+    (2, 3, 1, 4096, 4094, torch.float32, False),     # one row a block
+])
+def test_rope_narrow_halves_in_whole_rows(n, Hq, Hkv, D, rot, dtype, inter):
+    """Halves that are no multiples of 16 bytes in rows that are: against the definition, in place inside a wider row,
+    and bit for bit what the same rows give from an address that is not aligned."""
+    g = torch.Generator(device=DEV).manual_seed(n + rot)
+    q, k = (torch.randn(n, h, D, generator=g, device=DEV).to(dtype) for h in (Hq, Hkv))
+    pos = torch.randint(0, 1 << 20, (n,), generator=g, device=DEV)
+    freq, _ = tq.rope_frequencies(rot, 10000.0)
+    f = torch.tensor(freq, device=DEV)
+    qo, ko = tq.rope(q, k, pos, f, interleaved=inter)
+    _check(qo, _np(q), pos.cpu().numpy(), freq, inter, label="q")
+    _check(ko, _np(k), pos.cpu().numpy(), freq, inter, label="k")
+    for shift in (0, 1):
+        wide = torch.full((n, 16 + (Hq + Hkv) * D + 16), 7.0, device=DEV, dtype=dtype)
+        a = wide[:, 16 - shift:16 - shift + Hq * D].unflatten(1, (Hq, D))
+        b = wide[:, 16 - shift + Hq * D:16 - shift + (Hq + Hkv) * D].unflatten(1, (Hkv, D))
+        a.copy_(q)
+        b.copy_(k)
+        tq.rope(a, b, pos, f, interleaved=inter, q_out=a, k_out=b)
+        assert torch.equal(a, qo) and torch.equal(b, ko), shift
+        assert (wide[:, :16 - shift] == 7).all() and (wide[:, 16 - shift + (Hq + Hkv) * D:] == 7).all()
+
+
+@gpu
 def test_rope_far_positions():
     """Positions up to 2^31 in 32 bits and 2^40 in 64: the angle keeps 64-bit turns.  The product pos * freq / 2 pi is
     rounded twice (2^-52 relative), which at 2^40 turns / 2 pi is 2 pi 2^-14.6 of an angle; at 2^31 2 pi 2^-23.6."""
