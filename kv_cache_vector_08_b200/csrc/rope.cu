@@ -13,7 +13,7 @@
 // Bound: HBM (every element is read and written once).  A thread moves one vector of each
 // half of the pairs (half layout) or two adjacent ones (interleaved) at a time; queries and
 // keys go in one launch, since for a decode step the launch is the cost.  32,768 tokens of 32 + 8 heads
-// of 128 channels (bf16, 671 MB): 115 us, 5.8 TB/s, 0.89 of a copy's rate; 64 tokens: 2.4 us.
+// of 128 channels (bf16, 671 MB): 111 us, 6.0 TB/s, 0.92 of a copy's rate; 64 tokens: 2.3 us.
 #include <algorithm>
 #include <cmath>
 
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const __grid_cons
   };
   // The thread's first unit is on its way while the angles are formed.  (One unit at a time and many
   // warps: four units a thread need 126 registers, and with 16 warps an SM the 32K prompt took 218 us; two
-  // units, 32 warps: 134 us; one, 32 or 40 warps: 127 and 125 us; 48 spill: 127 us.)
+  // units, 32 warps: 134 us; one, 32 or 40 warps: 127 and 125 us; 48 spill: 127 us; later steps took the 40 to 111.)
   Unit x;
   int u = u0 + threadIdx.x;
   if (u < u1) fetch(u, x);
@@ -253,9 +253,9 @@ int launch_v(RopeArgs A, int heads, bool inter, int sms, cudaStream_t st) {
   const int per_head = A.rot_units + (A.D - A.rot) / V;
   A.per_head = Div(per_head);
   A.per_tok = Div(per_head * heads);
-  // A block takes about four units a thread: whole tokens (their sines are shared by the
-  // heads), or, when the tokens are too few for the device, slices of one token's heads.
-  const int want = 4 * kRopeThreads;
+  // A block takes about eight units a thread (the 32K prompt with cold caches: two 152 us, four 121, eight
+  // and twelve 119): whole tokens (their sines are shared by the heads), or, when the tokens are too few for the device, slices of one token's heads.
+  const int want = 8 * kRopeThreads;
   int64_t tb = std::max<int64_t>(1, want / A.per_tok.d);
   tb = std::max<int64_t>(1, std::min<int64_t>(tb, A.n / (4 * sms)));
   tb = std::min<int64_t>(tb, std::max(1, 24 * 1024 / std::max(1, A.rot / 2 * (int)sizeof(float2))));
