@@ -166,16 +166,19 @@ struct MmaArgs {
   uint32_t piv_bytes[2];   // into L2 at the start of this kernel
   const int32_t* table;    // paged cache: physical page of (sequence, logical page), or NULL
   int page, max_pages;     // tokens per page (a multiple of the 64-token stage), pages per sequence
+  int await_inputs;        // seq_lens and table are written by the launch in front (page selection)
   int64_t npages;          // physical pages the caches hold (min over the groups' caches)
 };
 
 // First cache slot of the 64-token stage starting at token ts of (sequence b, kv head hk).
 // Contiguous caches: slot0 + ts.  Paged caches: page p of the pool holds kv head hk's
 // tokens in slots (p Hkv + hk) page .. + page - 1; a stage never crosses a page.  A page
-// index outside the pool reads page 0 and is reported as device error 901.
+// index outside the pool reads page 0 and is reported as device error 901.  (A plain load: the
+// table may have been written by the launch in front while this grid was already there, which the
+// read-only path is not for.)
 __device__ __forceinline__ int64_t stage_slot(const MmaArgs& A, int b, int hk, int ts, int64_t slot0) {
   if (!A.table) return slot0 + ts;
-  int pg = __ldg(A.table + (size_t)b * A.max_pages + ts / A.page);
+  int pg = A.table[(size_t)b * A.max_pages + ts / A.page];
   if (pg < 0 || pg >= A.npages) {
     if (A.err) atomicCAS(A.err, 0, (int)kErrSlotRange);
     pg = 0;
@@ -211,12 +214,12 @@ __device__ __forceinline__ void load_qops(QOps<GC>& f, const MmaArgs& A, int gi,
   const float* ps = pm + A.D;
   // fixed-point scale of each (head, part) row: 32000 / max |v| over the group's
   // coordinates (the four threads of a quad hold the head's d_g coordinates); all of the
-  // thread's values are loaded in one round
+  // thread's values are loaded in one round (plain loads, as of all that the launches in front write)
   float4 va[GC::CQ / 4], vc[GC::CQ / 4];
 #pragma unroll
   for (int u = 0; u < GC::CQ / 4; ++u) {
-    va[u] = __ldg(reinterpret_cast<const float4*>(pm) + u);
-    vc[u] = __ldg(reinterpret_cast<const float4*>(ps) + u);
+    va[u] = reinterpret_cast<const float4*>(pm)[u];
+    vc[u] = reinterpret_cast<const float4*>(ps)[u];
   }
   float mm = 0.f, ms = 0.f;
 #pragma unroll
@@ -391,6 +394,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, TQ_DECODE_CTAS_PER_SM) deco
   const int b = bh / A.Hkv, hk = bh % A.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, l = lane & 3;
+  // This grid may start before the memory of the launch in front is visible to it, whether or not that
+  // launch triggers it early.  Behind the query projection only the consumers read its results (they
+  // wait below); behind the page selection every thread reads its lengths and the producer its table.
+  if (A.await_inputs) grid_dependency_wait();
   const int T = max(0, (int)min((int64_t)A.seq_lens[b], A.max_len));
   const int t_begin = split * A.chunk;
   const int t_end = min(T, t_begin + A.chunk);
@@ -1229,6 +1236,7 @@ int launch_decode_mma(const tq_ctx* const* kctx, const tq_ctx* const* vctx, cons
   }
   A.err = kctx[0]->dev_err;
   A.table = table;
+  A.await_inputs = view.prepared ? 1 : 0;
   if (table) {
     A.page = page;
     A.max_pages = (int)(max_len / page);

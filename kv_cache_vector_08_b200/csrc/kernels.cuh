@@ -24,7 +24,9 @@ DecodeWs decode_ws(int B, int Hq, int Hkv, int D, int G, int64_t max_len);
 struct DecodeView {
   int out_dtype = TQ_DTYPE_F32;
   int perm_Hq = 0, perm_Hkv = 0;   // 0: the call's own
-  bool prepared = false;           // launch_decode_prep ran already (kernels in between launch early)
+  // launch_decode_prep ran already, and the launch directly in front writes seq_lens and the table: the
+  // decode kernel reads neither before its grid-dependency wait
+  bool prepared = false;
 };
 size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D, int ngroups, int64_t max_len, int qp_ld);
 int launch_dequantize_tc(const tq_ctx* ctx, const tq_packed* src, const int64_t* slots, int64_t n, float* out,

@@ -14,7 +14,8 @@
 //
 // The chosen pages become a block table per (sequence, kv head): page p of kv head hk holds
 // slots (p Hkv + hk) page .., so it is page p Hkv + hk of a cache with one kv head, and the
-// decode kernels run on B Hkv sequences of one kv head each, unchanged.
+// decode kernels run on B Hkv sequences of one kv head each.  The decode kernel starts early, so
+// it waits for this selection before it reads a length or the table.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
