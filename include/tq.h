@@ -443,10 +443,16 @@ int tq_sparse_decode_attention(const tq_ctx* const* kctx, const tq_ctx* const* v
  * changes.
  * q, out: device [B][T][Hq][D] of q_dtype (F32, BF16, F16), 16-byte aligned (and channel_perm); 1 <= T <= 256.  draft_lens: device int32 [B],
  * clamped to [0, min(T, seq_lens[b])], or NULL: T each.  tree_mask: device uint64 [B][T][(T+63)/64], or
- * NULL: a chain (row j attends the drafted tokens up to j).  The products run on fp16 operands with
- * 32-bit sums, so an F32 result is good to about 1e-3 as well.  Supported caches, other arguments,
+ * NULL: a chain (row j attends the drafted tokens up to j).  Supported caches, other arguments,
  * layouts and errors as tq_decode_attention_ex (opts may be NULL); TQ_ERR_UNSUPPORTED for T outside
- * [1, 256]. */
+ * [1, 256].
+ * Precision: the products run on fp16 operands (queries and outputs scaled row by row, norms multiplied
+ * into keys and values) with 32-bit sums and softmax, so an F32 result is no better than an F16 one:
+ * about 1e-3 of the row, as long as
+ *   - scale |q| |k| is up to about 30: a logit's error is about 4e-4 scale |q| |k| / sqrt(D), and that is
+ *     its weight's relative error;
+ *   - the value norms that count are 3e-4 or more: a smaller one leaves its elements fewer bits (norms of
+ *     1e-4: 2e-3 of the row, of 1e-5: 2e-2). */
 size_t tq_tree_workspace_size(int B, int T, int Hq, int Hkv, int D, int ngroups, int64_t max_len);
 int tq_tree_attention(const tq_ctx* const* kctx, const tq_ctx* const* vctx, const int* group_off, int ngroups,
                       const void* q, int q_dtype, const tq_packed* kcache, const tq_packed* vcache,

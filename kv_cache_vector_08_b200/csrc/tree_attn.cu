@@ -27,8 +27,8 @@
 // Rows that fill a half or a quarter of the 128 lanes are repeated in the others (fold 2 or 4), and
 // each copy takes its half or quarter of the tile's columns, with zeros in the rest of its P.  The
 // products cost the same, the exponentials spread over all lanes.  The copies' sums meet at the end.
-// At last O / l is rotated back by one more product, and written (one split) or left as a partial
-// for the merge kernel.
+// At last O / l, each row scaled by a power of two of its own as the queries are, is rotated back by
+// one more product, and written (one split) or left as a partial for the merge kernel.
 //
 // The levels of a codebook enter scaled by a factor for which fp16 holds them almost exactly
 // (tq_init looks for it); the projection and the last product take the factor out.
@@ -198,6 +198,13 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+
+// Exponent e in [-110, 110] that brings a row's largest element near 2^9, so that its fp16 operand keeps
+// eleven bits of whatever counts in the row (fp16 alone has a fixed step below 6e-5); 2^e as a float.
+__device__ __forceinline__ int row_exp(float mx) {
+  return mx > 0.f && mx < INFINITY ? max(-110, min(110, 136 - (int)(__float_as_uint(mx) >> 23))) : 0;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // Tokens of sequence b and the drafted ones among them.
 __device__ __forceinline__ void lens_of(const TreeArgs& A, int b, int& len, int& nd) {
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   Bars* bar = reinterpret_cast<Bars*>(smem + kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 512 - 8);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  float* s_scale = reinterpret_cast<float*>(smem + kOffMisc + 512);      // [128] logit scale of a lane's row
+  float* s_scale = reinterpret_cast<float*>(smem + kOffMisc + 512);      // [128] logit scale of a lane's row; at the end, what undoes its output's
   float2* s_ml = reinterpret_cast<float2*>(smem + kOffMisc + 1024);      // [128] the copies' maxima and sums
   // (a shuffle makes the warp's number, and what the products' addresses come from, known to be uniform: the
   // compiler then keeps the operands of the products in uniform registers)
@@ -595,15 +602,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      // 2^e as a float, e in [-110, 110]
-      const int e = mx > 0.f && mx < INFINITY ? max(-110, min(110, 136 - (int)(__float_as_uint(mx) >> 23))) : 0;
-      const float up = A.sign * __uint_as_float((uint32_t)(127 + e) << 23);
+      const int e = row_exp(mx);
+      const float up = A.sign * pow2(e);
       const uint2 h = make_uint2(h2_bits(v.x * up, v.y * up), h2_bits(v.z * up, v.w * up));
 #pragma unroll 1
       for (int c = r; c < kRows; c += per) {
         *reinterpret_cast<uint2*>(smem + (lane >> 4) * (kRows * 128) + swz(c, (lane >> 1) & 7) + 8 * (lane & 1)) = h;
         // (not 0: a column left out is -inf before the scale)
-        if (lane == 0) s_scale[c] = fmaxf(A.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1e-30f);
+        if (lane == 0) s_scale[c] = fmaxf(A.scale_log2 * pow2(-e), 1e-30f);
       }
     }
     fence_proxy_async_smem();
@@ -816,7 +822,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     if (ok) {
       tc_fence_after();
       if (warp_live) {
-        const float inv = L > 0.f || L != L ? w / L : 0.f;
+        float inv = L > 0.f || L != L ? w / L : 0.f, mx = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lane_base + kColO + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(__uint_as_float(o[e])));
+        }
+        const int up = row_exp(mx * inv);
+        inv *= pow2(up);
+        s_scale[threadIdx.x] = pow2(-up);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32], x[16];
@@ -938,7 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll 1
       for (int c = r; c < kRows; c += per) {
         const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + kOffSum) + c * kSumLd + 4 * lane);
-        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+        const float f = s_scale[c];
+        v = make_float4(fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w));
       }
       v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     }
