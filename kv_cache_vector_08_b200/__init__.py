@@ -533,6 +533,16 @@ class _CachePlan:
         self._vc = (_Packed * G)(*[p.struct() for p in vcache])
         self._keep = (kctx, vctx, kcache, vcache)
         self.device = kcache[0].codes.device
+        self._streams = {_raw_stream(None)}          # where the plan's own tensors are at home, or recorded
+
+    def _used_on(self, stream, *own):
+        """The plan may be dropped while a call runs: its tensors' memory is then not to be used again before the call's
+        stream, the given or the current one, is through with it."""
+        raw = _raw_stream(stream)
+        if raw not in self._streams:
+            for t in own:
+                t.record_stream(stream if stream is not None else _torch().cuda.current_stream())
+            self._streams.add(raw)
 
     def _workspace(self, need):
         return _torch().empty(max(need, 1), dtype=_torch().uint8, device=self.device)
@@ -545,8 +555,6 @@ class _CachePlan:
     def _query(self, q, shape, out, stream):
         if q.shape != shape:
             raise ValueError("q must be %s, got %s" % (shape, tuple(q.shape)))
-        if stream is not None:
-            self.workspace.record_stream(stream)     # (the plan may be dropped while the call runs)
         if out is None or not q.is_contiguous():
             with _on(stream):
                 q = q.contiguous()
@@ -587,8 +595,7 @@ class SparsePlan(_CachePlan):
     def __call__(self, q, bounds, seq_lens, scale: float, out=None, stream=None):
         """q [B, Hq, D] -> (out [B, Hq, D] of q's dtype, selected int32 [B, Hkv, select]: the plan's own tensor)."""
         q, out = self._query(q, (self.B, self.Hq, self.D), out, stream)
-        if stream is not None:
-            self.selected.record_stream(stream)
+        self._used_on(stream, self.workspace, self.selected)
         if bounds.dim() != 4 or bounds.shape[1:] != (self.Hkv, 2, self.D) or not bounds.is_contiguous():
             raise ValueError("bounds must be contiguous [pages, Hkv, 2, D]")
         _int32(seq_lens, (self.B,), "seq_lens")
@@ -655,6 +662,7 @@ class TreePlan(_CachePlan):
         [B, T, ceil(T / 64)] (tree_mask) or None (a chain)."""
         torch = _torch()
         q, out = self._query(q, (self.B, self.T, self.Hq, self.D), out, stream)
+        self._used_on(stream, self.workspace)
         _int32(seq_lens, (self.B,), "seq_lens")
         if draft_lens is not None:
             _int32(draft_lens, (self.B,), "draft_lens")
