@@ -448,8 +448,12 @@ def rope(q, k, positions, freqs, *, interleaved: bool = False, factor: float = 1
          q_out=None, k_out=None, stream=None):
     """Rotary positions of q [n, Hq, D] and k [n, Hkv, D] (k may be None) in one launch -> (q_out, k_out).
     positions int32 / int64 CUDA [n]; freqs float64 CUDA [rot/2]; channels from rot on are copied.  The outputs may
-    be q and k themselves.  transpose=True turns back: the gradient of the call without it."""
+    be q and k themselves.  transpose=True turns back: the gradient of the call without it, which autograd takes where
+    q or k requires one (then without q_out and k_out; freqs get none)."""
     torch = _torch()
+    if q.requires_grad or freqs.requires_grad or (k is not None and k.requires_grad):
+        if torch.is_grad_enabled():
+            return _rope_with_gradient(q, k, positions, freqs, interleaved, factor, transpose, q_out, k_out, stream)
     if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous float64 tensor [rot/2]")
     n, wide = q.shape[0], positions.dtype is torch.int64
@@ -468,6 +472,49 @@ def rope(q, k, positions, freqs, *, interleaved: bool = False, factor: float = 1
     return q_out, k_out
 
 
+def _rope_with_gradient(q, k, positions, freqs, interleaved, factor, transpose, q_out, k_out, stream):
+    if q_out is not None or k_out is not None:
+        raise ValueError("q_out and k_out cannot be given where q or k requires a gradient")
+    if freqs.requires_grad:
+        raise ValueError("freqs must not require a gradient: none is formed for them")
+    with _on(stream):           # (autograd runs a backward pass on the stream that was current in the forward pass)
+        y = _rope_function().apply(q, k, positions, freqs, interleaved, factor, transpose)
+    return y if k is not None else (y, None)
+
+
+def _rope_function():
+    global _RopeFunction
+    if _RopeFunction is None:
+        torch = _torch()
+
+        class _RopeFunction(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, positions, freqs, interleaved, factor, transpose):
+                ctx.save_for_backward(positions, freqs)
+                ctx.how = interleaved, factor, transpose
+                ctx.set_materialize_grads(False)
+                q_out, k_out = rope(q, k, positions, freqs, interleaved=interleaved, factor=factor, transpose=transpose)
+                if k is None:
+                    return q_out
+                ctx.mark_non_differentiable(*(y for y, need in zip((q_out, k_out), ctx.needs_input_grad) if not need))
+                return q_out, k_out
+
+            @staticmethod
+            def backward(ctx, gq, gk=None):
+                # the transposed rotation of each gradient that is asked for, in one launch
+                positions, freqs = ctx.saved_tensors
+                interleaved, factor, transpose = ctx.how
+                gq, gk = (g if need else None for g, need in zip((gq, gk), ctx.needs_input_grad))
+                given = [g if g.stride(-1) == 1 else g.contiguous() for g in (gq, gk) if g is not None]
+                back = iter(())
+                if given:
+                    back = iter(rope(given[0], given[1] if len(given) > 1 else None, positions, freqs,
+                                     interleaved=interleaved, factor=factor, transpose=not transpose))
+                return (*(None if g is None else next(back) for g in (gq, gk)), None, None, None, None, None)
+    return _RopeFunction
+
+
+_RopeFunction = None
 _ROPE_SIDES = {n: struct.Struct("@" + n * "PPi4xqqqq") for n in (1, 2)}     # tq_rope_tensor, n times
 
 
@@ -485,9 +532,9 @@ def _rope_side(x, out, q, stream):
         raise ValueError("q, k and their outputs must be [n, heads, D] of one dtype")
     xt, xh, xc = x.stride()
     ot, oh, oc = out.stride()
-    if xc != 1 or oc != 1:
+    if (xc != 1 or oc != 1) and shape.numel():
         raise ValueError("q, k and their outputs must have unit stride along channels")
-    if (ot == 0 and shape[0] > 1) or (oh == 0 and shape[1] > 1):
+    if ((ot == 0 and shape[0] > 1) or (oh == 0 and shape[1] > 1)) and shape.numel():
         raise ValueError("an output must not be expanded")
     return out, (x.data_ptr(), out.data_ptr(), shape[1], xt, xh, ot, oh)
 
@@ -593,7 +640,8 @@ class SparsePlan(_CachePlan):
         self.workspace = self._workspace(sparse_workspace_size(B, Hq, Hkv, D, self.G, max_len, page_tokens, self.select))
 
     def __call__(self, q, bounds, seq_lens, scale: float, out=None, stream=None):
-        """q [B, Hq, D] -> (out [B, Hq, D] of q's dtype, selected int32 [B, Hkv, select]: the plan's own tensor)."""
+        """q [B, Hq, D] -> (out [B, Hq, D] of q's dtype, selected int32 [B, Hkv, select]: the plan's own tensor).
+        No gradient is formed, as for decode_attention."""
         q, out = self._query(q, (self.B, self.Hq, self.D), out, stream)
         self._used_on(stream, self.workspace, self.selected)
         if bounds.dim() != 4 or bounds.shape[1:] != (self.Hkv, 2, self.D) or not bounds.is_contiguous():
@@ -659,7 +707,7 @@ class TreePlan(_CachePlan):
 
     def __call__(self, q, seq_lens, draft_lens, mask, scale: float, out=None, stream=None):
         """q [B, T, Hq, D] -> out of its shape and dtype.  draft_lens int32 [B] or None (T each); mask int64
-        [B, T, ceil(T / 64)] (tree_mask) or None (a chain)."""
+        [B, T, ceil(T / 64)] (tree_mask) or None (a chain).  No gradient is formed, as for decode_attention."""
         torch = _torch()
         q, out = self._query(q, (self.B, self.T, self.Hq, self.D), out, stream)
         self._used_on(stream, self.workspace)
