@@ -396,7 +396,8 @@ int tq_rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* 
  * least the largest number of new rows of a sequence (it sizes the launch; more rows than that are
  * still taken, only slower).  block_table: device int32 [B][max_pages]; the pages of two sequences
  * that append in one call must differ.  A token past max_pages, or in a page outside [0, npages), is
- * left out, and a sequence whose rows are not all in [0, n) as a whole.  NaN elements are skipped.
+ * left out, and a sequence whose rows are not all in [0, n) as a whole.  NaN elements are skipped; a
+ * channel in which a page has no others holds (+infinity, -infinity).
  * Errors: TQ_ERR_INVALID_ARG (NULL pointers, bad sizes or dtype), TQ_ERR_UNSUPPORTED (D > 256, B or
  * Hkv > 65535, a pointer that is not aligned to its element), TQ_ERR_CUDA. */
 int tq_page_bounds(const void* k, int64_t n, int dtype, int64_t k_token, int64_t k_head, const int32_t* cu_new,
@@ -405,8 +406,12 @@ int tq_page_bounds(const void* k, int64_t n, int dtype, int64_t k_token, int64_t
 
 /* tq_sparse_decode_attention -- one decode step over the pages that a score selects: page p of
  * sequence b scores, for kv head h,
- *   sum over its query heads and channels of max(q_c lo_c, q_c hi_c)     (sums in 64 bits)
- * and the `select` pages with the highest scores are attended as by tq_decode_attention, the first
+ *   sum over the channels c of  q+_c hi_c + q-_c lo_c                     (sums in 64 bits)
+ * q+_c and q-_c: the sums over its query heads of max(q_c, 0) and min(q_c, 0); a product with a sum of 0
+ * is 0.  For lo <= hi, as tq_page_bounds keeps them, that is the sum over the heads and channels of
+ * max(q_c lo_c, q_c hi_c).  Where all keys of a page are NaN in a channel, tq_page_bounds leaves
+ * (+infinity, -infinity), bounds of no key at all: a query that is not 0 there makes the score -infinity.
+ * The `select` pages with the highest scores are attended as by tq_decode_attention, the first
  * `first` and last `last` pages of the sequence in any case; equal scores go to the lower page, a
  * NaN score comes last.  A sequence with at most `select` pages attends all of them.
  * selected (device int32 [B][Hkv][select], may be NULL): the attended pages (logical numbers) in

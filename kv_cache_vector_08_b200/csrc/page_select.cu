@@ -7,7 +7,10 @@
 //   score(page) = sum over the kv head's query heads h and channels c of
 //     max(q_hc lo_c, q_hc hi_c), an upper bound of the summed inner products with any key of
 //     the page.  With lo <= hi this is sum_c (q+_c hi_c + q-_c lo_c), q+ and q- the sums of the
-//     heads' positive and negative parts: two products a channel, whatever the head count.
+//     heads' positive and negative parts: two products a channel, whatever the head count.  The
+//     second form is what is computed, and stands for the empty box as well: a channel in which
+//     every key was NaN holds (+inf, -inf), and gives -inf, the bound over no key, where the first
+//     form would give +inf.
 //     Sums run in 64 bits, so that the choice does not hang on a rounding order.
 //   selected = the `select` pages with the highest scores (ties to the lower page), the first
 //     and last pages of a sequence in any case, in ascending order.
