@@ -580,6 +580,8 @@ class _CachePlan:
         self._vc = (_Packed * G)(*[p.struct() for p in vcache])
         self._keep = (kctx, vctx, kcache, vcache)
         self.device = kcache[0].codes.device
+        for p in (*kcache, *vcache):
+            self._same_device(p.codes, p.norm, p.rnorm)
         self._streams = {_raw_stream(None)}          # where the plan's own tensors are at home, or recorded
 
     def _used_on(self, stream, *own):
@@ -647,7 +649,7 @@ class SparsePlan(_CachePlan):
         if bounds.dim() != 4 or bounds.shape[1:] != (self.Hkv, 2, self.D) or not bounds.is_contiguous():
             raise ValueError("bounds must be contiguous [pages, Hkv, 2, D]")
         _int32(seq_lens, (self.B,), "seq_lens")
-        _on_current_device(q, bounds, seq_lens, out)
+        _on_current_device(q, bounds, seq_lens, out, self.workspace)      # (the caches are where the workspace is)
         o = self._opts
         o.bounds, o.bounds_dtype, o.bounds_pages = bounds.data_ptr(), _dtype_code(bounds), bounds.shape[0]
         _check(lib().tq_sparse_decode_attention(
@@ -717,7 +719,7 @@ class TreePlan(_CachePlan):
         if mask is not None and (mask.dtype is not torch.int64 or not mask.is_contiguous()
                                  or mask.shape != (self.B, self.T, (self.T + 63) // 64)):
             raise ValueError("mask must be a contiguous int64 tensor [B, T, ceil(T / 64)]")
-        _on_current_device(q, seq_lens, draft_lens, mask, out)
+        _on_current_device(q, seq_lens, draft_lens, mask, out, self.workspace)      # (the caches are where the workspace is)
         _check(lib().tq_tree_attention(
             self._k, self._v, self._off, self.G, q.data_ptr(), _dtype_code(q), self._kc, self._vc, seq_lens.data_ptr(),
             None if draft_lens is None else draft_lens.data_ptr(), None if mask is None else mask.data_ptr(), self.B, self.T, self.Hq, self.Hkv, self.D, self.max_len, scale, out.data_ptr(),

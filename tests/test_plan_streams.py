@@ -90,3 +90,48 @@ def test_a_plan_dropped_while_its_call_runs_on_another_current_stream():
         torch.cuda.synchronize()
         assert torch.equal(s, want_s) and torch.equal(t, want_t) and kctx[0].device_error() == 0
         del junk
+
+
+class _On:
+    """A tensor that says it is on another GPU."""
+
+    def __init__(self, t, index):
+        self.t, self.device = t, torch.device("cuda", index)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.device.index
+
+
+@pytest.mark.parametrize("which", ["sparse", "tree"])
+def test_caches_of_another_device_are_refused(monkeypatch, which):
+    """Caches of which one lies elsewhere, and a call with another device current than the caches': before anything
+    runs."""
+    monkeypatch.setattr(tq, "lib", lambda: types.SimpleNamespace(tq_sparse_workspace_size=lambda *a: 256,
+                                                                 tq_tree_workspace_size=lambda *a: 256))
+    monkeypatch.setattr(tq, "_raw_stream", lambda stream: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    i32 = _On(torch.zeros(1, dtype=torch.int32), 0)
+    table = torch.zeros(1, 1, dtype=torch.int32)
+    q, bounds = _On(torch.zeros(1, 2, D), 0), _On(torch.zeros(1, 1, 2, D), 0)
+    qt = _On(torch.zeros(1, 3, 2, D), 0)
+
+    def plan(*args):
+        if which == "sparse":
+            return tq.SparsePlan(*args, 1, 2, 1, D, 64, block_table=table, page_tokens=64, select=1)
+        return tq.TreePlan(*args, 1, 3, 2, 1, D, 64)
+
+    for i in (3, 4):
+        for part in ("codes", "norm", "rnorm"):
+            args = _caches()
+            setattr(args[i][0], part, _On(getattr(args[i][0], part), 1))
+            with pytest.raises(ValueError):
+                plan(*args)
+    p = plan(*_caches())                                        # (on the host: not on the current device)
+    with pytest.raises(ValueError, match="cpu"):
+        if which == "sparse":
+            p(q, bounds, i32, 0.1, out=_On(torch.zeros(1, 2, D), 0))
+        else:
+            p(qt, i32, None, None, 0.1, out=_On(torch.zeros(1, 3, 2, D), 0))
