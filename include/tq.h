@@ -347,7 +347,8 @@ int tq_search_topk(const tq_ctx* ctx, const float* q, int64_t nq, const tq_packe
  * with (x1, x2) = channels (i, i + rot/2), or (2i, 2i + 1) with TQ_ROPE_INTERLEAVED; channels
  * rot..D-1 are copied.  TQ_ROPE_TRANSPOSE turns by -a: the gradient of the call without it (and,
  * for factor 1, its inverse).  The angle is formed in 64 bits, the products in 32 bits, and the
- * result is rounded once to the tensors' type.
+ * result is rounded once to the tensors' type.  The angle is good to 1e-7 for positions up to 2^25, to
+ * 5e-7 at 2^31, and beyond in proportion to the position.
  * tensors: host array of ntensors (1 or 2); x and out device, of dtype (F32 / BF16 / F16), channel
  *   c of head h of token v at x + v*x_token + h*x_head + c (elements; channels are contiguous).
  *   out may be x with the same strides; any other overlap is undefined.

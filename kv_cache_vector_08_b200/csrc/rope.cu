@@ -6,8 +6,10 @@
 // on are copied.  The transposed rotation (the gradient, and for f = 1 the inverse) turns by -a.
 //
 // The angle is formed in 64 bits as a number of turns, pos * (freq / 2 pi), of which only the
-// fraction is kept: positions of 2^31 still give the angle to 2e-7, where a 32-bit product
-// would be off by whole turns.  Its sine and cosine are taken once per token and pair of a
+// fraction is kept, in 32 bits: the angle is good to 1e-7 for positions up to 2^25, where that
+// rounding is all of it, to 5e-7 at 2^31 and from there on in proportion to the position (the
+// 64-bit product's own rounding; largest errors of 100,000 random angles against 60 digits).
+// A 32-bit product would be off by whole turns.  Its sine and cosine are taken once per token and pair of a
 // block, in shared memory, and serve all heads of both tensors.
 //
 // Bound: HBM (every element is read and written once).  A thread moves one vector of each
