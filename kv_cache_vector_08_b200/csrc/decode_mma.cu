@@ -1153,6 +1153,8 @@ float mmaops::host_luts(const tq_ctx* kc, const tq_ctx* vc, Luts* t) {
     t->kh[code / 4] |= (uint32_t)(uint8_t)hi << (8 * (code % 4));
     t->kl[code / 4] |= (uint32_t)(uint8_t)lo << (8 * (code % 4));
   }
+  // A value level is rounded once, to fp16 (2^-11 at most: 2e-4 of an output, the largest error of the
+  // kernel at ordinary logits).  A low part would double the value products.
   const Codebook& vb = vc->cb;
   const int half = vb.K / 2;
   for (int m = 0; m < half && m < 8; ++m) {

@@ -33,6 +33,16 @@
 // The levels of a codebook enter scaled by a factor for which fp16 holds them almost exactly
 // (tq_init looks for it); the projection and the last product take the factor out.
 //
+// Roundings: every operand is fp16 (2^-11), whatever the queries' type; sums, logits, maxima and sums of
+// the softmax are 32-bit.  What each operand costs, alone, of a row's size in a model of the arithmetic (3
+// bits, 4,096 tokens, normal queries at scale 1 / sqrt(128)): keys 6.3e-4 (level times norm, and one product of both
+// norms a token), the high halves of Pi and S 4.0e-4, projected queries 3.8e-4, rows before the rotation
+// back 2.1e-4, that rotation's high half 2.1e-4, values 1.8e-4, weights 0.6e-4, query rows 0 from 16 bits;
+// together 9.3e-4.  They are kept because the large ones are the tile's own operands: low halves of keys
+// and queries would make S three products, 1,536 cycles a tile where it has 512 (and the tile 1,370),
+// while low halves of the matrices and the output alone would leave 8.6e-4.  A bf16 result is rounded by
+// 1.7e-3 of its size in any case.
+//
 // P carries a factor 2^3: between the 2^15 it can reach (2^12 before the maximum moves) and the smallest
 // fp16, weights down to 2^-27 of the row's largest count at least.
 //
