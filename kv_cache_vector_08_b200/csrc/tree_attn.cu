@@ -63,6 +63,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "elem.cuh"
 #include "kernels.cuh"
 #include "mma_ops.cuh"
 #include "sm100.cuh"
@@ -129,37 +130,17 @@ struct TreeArgs {
   int* err;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
-template <typename T>
-struct alignas(4 * sizeof(T)) Four {
-  T v[4];
-};
 // Four consecutive channels 4 lane .. of an output row, or (perm: the kv head's permutation) the
 // channels that the row's group coordinates 4 lane .. stand for.
 template <typename T>
 __device__ __forceinline__ void store_row(T* row, const int32_t* perm, int lane, float4 v) {
-  Four<T> x;
+  Vec<T, 4> x;
   x.v[0] = from_f<T>(v.x);
   x.v[1] = from_f<T>(v.y);
   x.v[2] = from_f<T>(v.z);
   x.v[3] = from_f<T>(v.w);
   if (!perm) {
-    *reinterpret_cast<Four<T>*>(row + 4 * lane) = x;
+    *reinterpret_cast<Vec<T, 4>*>(row + 4 * lane) = x;
     return;
   }
   const int4 to = __ldg(reinterpret_cast<const int4*>(perm) + lane);
