@@ -395,7 +395,7 @@ int tq_rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* 
  * (device int32; rows of channel c and kv head h at k + row*k_token + h*k_head + c).  A page whose
  * first token is among them starts anew; any other keeps its bounds and widens them.  max_new: at
  * least the largest number of new rows of a sequence (it sizes the launch; more rows than that are
- * still taken, only slower).  block_table: device int32 [B][max_pages]; the pages of two sequences
+ * still taken, only slower; 0: there are none, and nothing is launched).  block_table: device int32 [B][max_pages]; the pages of two sequences
  * that append in one call must differ.  A token past max_pages, or in a page outside [0, npages), is
  * left out, and a sequence whose rows are not all in [0, n) as a whole.  NaN elements are skipped; a
  * channel in which a page has no others holds (+infinity, -infinity).

@@ -50,8 +50,8 @@
 // up to 128), the shared memory 768 (K and V written once, read once by the products), the issue slots 810
 // and the integer pipe of decoders and softmax 690; each waits on the others.  Products alone took 1,030
 // cycles a tile, decoders alone 1,160.  64 sequences of up to 8,192 tokens, 16 drafts, 8 kv heads of 4
-// query heads: 363 us (134 GFLOP, 412 MB; the first kernel of this shape, with one tile in flight, 723 us).
-// One sequence of 131,072 tokens, 63 drafts: 249 us, 203 GFLOP, 0.82 PFLOP/s.
+// query heads: 362 us (134 GFLOP, 412 MB; the first kernel of this shape, with one tile in flight, 723 us).
+// One sequence of 131,072 tokens, 63 drafts: 248 us, 203 GFLOP, 0.82 PFLOP/s.
 // Tried: two warps for the products, S and P V (391 us, spills); two softmax groups of two S buffers each
 // (404 us); four decoder sets (no change).
 //
