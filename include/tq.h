@@ -347,8 +347,8 @@ int tq_search_topk(const tq_ctx* ctx, const float* q, int64_t nq, const tq_packe
  * with (x1, x2) = channels (i, i + rot/2), or (2i, 2i + 1) with TQ_ROPE_INTERLEAVED; channels
  * rot..D-1 are copied.  TQ_ROPE_TRANSPOSE turns by -a: the gradient of the call without it (and,
  * for factor 1, its inverse).  The angle is formed in 64 bits, the products in 32 bits, and the
- * result is rounded once to the tensors' type.  The angle is good to 1e-7 for positions up to 2^25, to
- * 5e-7 at 2^31, and beyond in proportion to the position.
+ * result is rounded once to the tensors' type.  For frequencies up to 1 the angle is good to 1e-7 at
+ * positions up to 2^25, to 5e-7 at 2^31, and beyond in proportion to the position.
  * tensors: host array of ntensors (1 or 2); x and out device, of dtype (F32 / BF16 / F16), channel
  *   c of head h of token v at x + v*x_token + h*x_head + c (elements; channels are contiguous).
  *   out may be x with the same strides; any other overlap is undefined.
@@ -395,8 +395,8 @@ int tq_rope_frequencies(int rot, double base, const tq_rope_scaling* s, double* 
  * (device int32; rows of channel c and kv head h at k + row*k_token + h*k_head + c).  A page whose
  * first token is among them starts anew; any other keeps its bounds and widens them.  max_new: at
  * least the largest number of new rows of a sequence (it sizes the launch; more rows than that are
- * still taken, only slower; 0: there are none, and nothing is launched).  block_table: device int32 [B][max_pages]; the pages of two sequences
- * that append in one call must differ.  A token past max_pages, or in a page outside [0, npages), is
+ * still taken, only slower; 0: there are none, and nothing is launched).  block_table: device int32
+ * [B][max_pages]; the pages of two sequences that append in one call must differ.  A token past max_pages, or in a page outside [0, npages), is
  * left out, and a sequence whose rows are not all in [0, n) as a whole.  NaN elements are skipped; a
  * channel in which a page has no others holds (+infinity, -infinity).
  * Errors: TQ_ERR_INVALID_ARG (NULL pointers, bad sizes or dtype), TQ_ERR_UNSUPPORTED (D > 256, B or

@@ -6,11 +6,11 @@
 // on are copied.  The transposed rotation (the gradient, and for f = 1 the inverse) turns by -a.
 //
 // The angle is formed in 64 bits as a number of turns, pos * (freq / 2 pi), of which only the
-// fraction is kept, in 32 bits: the angle is good to 1e-7 for positions up to 2^25, where that
-// rounding is all of it, to 5e-7 at 2^31 and from there on in proportion to the position (the
-// 64-bit product's own rounding; largest errors of 100,000 random angles against 60 digits).
-// A 32-bit product would be off by whole turns.  Its sine and cosine are taken once per token and pair of a
-// block, in shared memory, and serve all heads of both tensors.
+// fraction is kept, in 32 bits: for frequencies up to 1 the angle is good to 1e-7 at positions up
+// to 2^25, where that rounding is all of it, to 5e-7 at 2^31 and from there on in proportion to the
+// position (the 64-bit product's own rounding; largest errors of 100,000 random angles against 60
+// digits).  A 32-bit product would be off by whole turns.  Its sine and cosine are taken once per
+// token and pair of a block, in shared memory, and serve all heads of both tensors.
 //
 // Bound: HBM (every element is read and written once).  A thread moves one vector of each
 // half of the pairs (half layout) or two adjacent ones (interleaved) at a time; queries and

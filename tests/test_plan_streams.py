@@ -1,4 +1,5 @@
 """Plans of the calls around the cache: their own memory on the streams that use it."""
+import contextlib
 import types
 
 import pytest
@@ -26,7 +27,7 @@ def host(monkeypatch):
     monkeypatch.setattr(tq, "lib", lambda: fake)
     monkeypatch.setattr(tq, "_raw_stream", lambda stream: (state.current if stream is None else stream).cuda_stream)
     monkeypatch.setattr(tq, "_on_current_device", lambda *t: None)
-    monkeypatch.setattr(tq, "_on", lambda stream: __import__("contextlib").nullcontext())
+    monkeypatch.setattr(tq, "_on", lambda stream: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: state.current)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: state.log.append((t.data_ptr(), s.cuda_stream)))
     return state
